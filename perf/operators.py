@@ -148,7 +148,7 @@ def _quantize(x):
     """[..., 64] bf16 -> codes [..., 64] and pairs [..., 2] (bf16)."""
     x = x.float()
     lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
-    s = (hi / 15 - lo / 15).bfloat16()
+    s = ((hi.double() - lo.double()) / 15).float().bfloat16()
     step = torch.where(s == 0, torch.ones_like(s), s).double()  # 64 bits: quotients next to a half
     n = ((x.double() - lo.double()) / step).round().clamp(0, 15)
     n = torch.where(s == 0, torch.zeros_like(n), n)
