@@ -382,6 +382,39 @@ vs_status vs_dense_attn_fwd(const void* Q, const void* K, const void* V, vs_dtyp
                             cudaStream_t stream);
 
 /*
+ * vs_window_attn_fwd / vs_window_attn_fwd_varlen -- causal sliding-window
+ * attention in which the first keys stay visible: the local-attention layers
+ * next to the vertical-slash ones (a window is every slash offset below
+ * `window`, the first keys are the vertical columns below `sinks`), without
+ * index sets, plan or bitmaps.  Query i of a sequence attends to
+ *     K_i = { j <= i : i - j < window  or  j < sinks },
+ * each key once; O and lse as for vs_sparse_attn_fwd (a row is never empty:
+ * it sees itself).
+ *   window   1 .. INT_MAX; at N or above the attention is dense causal.
+ *   sinks    0 .. INT_MAX first keys of each sequence (0: none).
+ *   Other arguments as for vs_dense_attn_fwd and vs_dense_attn_fwd_varlen
+ *            (a malformed cu_seqlens entry leaves that sequence's O rows
+ *            unwritten and sets VS_DEVFLAG_BOUNDS; rows of O and lse behind
+ *            the last sequence are left as they were).
+ *   ws       at least 256 bytes, 256-byte aligned (status word).
+ * VS_BF16 only (else VS_ERR_UNSUPPORTED); 1 <= N <= 2^24.
+ * What lies outside a sequence never reaches its rows, whatever it holds.
+ * Inside a sequence V must be finite: an infinity or NaN in V row j also
+ * reaches rows that do not see j but share its 128-key block (its weight is
+ * 0, and 0 * inf is NaN).  K may hold anything where it is not visible.
+ */
+vs_status vs_window_attn_fwd(const void* Q, const void* K, const void* V, vs_dtype dtype, int N,
+                             int Hq, int Hkv, int d, int64_t q_stride_tok, int64_t kv_stride_tok,
+                             float softmax_scale, int window, int sinks, void* O, float* lse,
+                             void* ws, size_t ws_bytes, cudaStream_t stream);
+vs_status vs_window_attn_fwd_varlen(const void* Q, const void* K, const void* V, vs_dtype dtype,
+                                    int total_tokens, int B, const int32_t* cu_seqlens,
+                                    int max_seqlen, int Hq, int Hkv, int d, int64_t q_stride_tok,
+                                    int64_t kv_stride_tok, float softmax_scale, int window,
+                                    int sinks, void* O, float* lse, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/*
  * vs_attn_aggregate -- ground-truth aggregation of the full causal attention
  * weights along vertical columns and slash diagonals: the indexer's
  * distillation target (Technical Summary, section 2, "Distillation Training":

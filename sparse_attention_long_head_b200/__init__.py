@@ -47,6 +47,7 @@ EXPORTS = (
     "vs_block_select_workspace_size_varlen", "vs_block_select_varlen",
     "vs_block_attn_workspace_size_varlen", "vs_block_sparse_attn_fwd_varlen",
     "vs_attn_aggregate_varlen", "vs_select_workspace_size_varlen", "vs_select_varlen",
+    "vs_window_attn_fwd", "vs_window_attn_fwd_varlen",
 )
 
 
@@ -125,6 +126,11 @@ def lib() -> ctypes.CDLL:
         L.vs_attn_aggregate_varlen.argtypes = [P, P, I, I, I, P, I, I, I, I, I64, I64, F, P, P,
                                                P, P, Z, P]
         L.vs_attn_aggregate_varlen.restype = I
+        L.vs_window_attn_fwd.argtypes = [P, P, P, I, I, I, I, I, I64, I64, F, I, I, P, P, P, Z, P]
+        L.vs_window_attn_fwd.restype = I
+        L.vs_window_attn_fwd_varlen.argtypes = [P, P, P, I, I, I, P, I, I, I, I, I64, I64, F, I, I,
+                                                P, P, P, Z, P]
+        L.vs_window_attn_fwd_varlen.restype = I
         L.vs_read_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
         L.vs_read_device_status.restype = I
         L.vs_selftest_wait_timeout.argtypes = [P, U64, P]
@@ -255,6 +261,28 @@ def vs_dense_attn_fwd(Q, K, V, O, lse, ws, softmax_scale=0.0, stream=None):
                                    Q.stride(0), K.stride(0), float(softmax_scale), _ptr(O),
                                    _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
            "vs_dense_attn_fwd")
+
+
+def vs_window_attn_fwd(Q, K, V, window, sinks, O, lse, ws, softmax_scale=0.0, stream=None):
+    """Sliding window of `window` keys with the first `sinks` keys visible; lse fp32 [Hq, N] or
+    None; ws of 256 bytes."""
+    N, Hq, d = Q.shape
+    Hkv = K.shape[1]
+    _check(lib().vs_window_attn_fwd(_ptr(Q), _ptr(K), _ptr(V), _dtype(Q), N, Hq, Hkv, d,
+                                    Q.stride(0), K.stride(0), float(softmax_scale), int(window),
+                                    int(sinks), _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
+                                    _stream(stream)), "vs_window_attn_fwd")
+
+
+def vs_window_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, window, sinks, O, lse, ws,
+                              softmax_scale=0.0, stream=None):
+    T, Hq, d = Q.shape
+    Hkv = K.shape[1]
+    B = cu_seqlens.numel() - 1
+    _check(lib().vs_window_attn_fwd_varlen(
+        _ptr(Q), _ptr(K), _ptr(V), _dtype(Q), T, B, _ptr(cu_seqlens), int(max_seqlen), Hq, Hkv, d,
+        Q.stride(0), K.stride(0), float(softmax_scale), int(window), int(sinks), _ptr(O),
+        _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "vs_window_attn_fwd_varlen")
 
 
 def vs_attn_aggregate(Q, K, lse, A_v, A_s, ws, softmax_scale=0.0, stream=None):
@@ -469,6 +497,16 @@ def dense_attention(Q, K, V, ws=None, with_lse=True, stream=None):
     lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device) if with_lse else None
     ws = workspace(256, Q.device) if ws is None else ws
     vs_dense_attn_fwd(Q, K, V, O, lse, ws, stream=stream)
+    return O, lse
+
+
+def window_attention(Q, K, V, window, sinks=0, ws=None, with_lse=True, stream=None):
+    """Allocates outputs and runs vs_window_attn_fwd -> (O, lse)."""
+    N, Hq, d = Q.shape
+    O = torch.empty_like(Q)
+    lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device) if with_lse else None
+    ws = workspace(256, Q.device) if ws is None else ws
+    vs_window_attn_fwd(Q, K, V, window, sinks, O, lse, ws, stream=stream)
     return O, lse
 
 

@@ -510,6 +510,67 @@ vs_status vs_block_sparse_attn_fwd_varlen(const void* Q, const void* K, const vo
                          ws_bytes, stream);
 }
 
+static vs_status window_impl(const void* Q, const void* K, const void* V, vs_dtype dtype, int N,
+                             int B, int64_t total, const int32_t* cu, int Hq, int Hkv, int d,
+                             int64_t q_stride_tok, int64_t kv_stride_tok, float softmax_scale,
+                             int window, int sinks, void* O, float* lse, void* ws,
+                             size_t ws_bytes, cudaStream_t stream) {
+  vs_status st = check_attn_common(Q, K, V, dtype, N, Hq, Hkv, d, q_stride_tok, kv_stride_tok,
+                                   softmax_scale, O);
+  if (st != VS_OK) return st;
+  if (B < 1 || total < 1 || total > INT32_MAX || window < 1 || sinks < 0)
+    return VS_ERR_INVALID_ARG;
+  if (dtype != VS_BF16) return VS_ERR_UNSUPPORTED;
+  const PlanLayout L = PlanLayout::make(N, 1);  // tile and pair counts
+  // units (sequence, head, pair of query blocks) are counted in 32 bits
+  if ((int64_t)B * Hq * L.P >= ((int64_t)1 << 31)) return VS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < kStatusBytes || !aligned(ws, 256)) return VS_ERR_WORKSPACE;
+  AttnArgs a{};
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.O = O;
+  a.lse = lse;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.H_sel = 1;
+  a.B = B;
+  a.total = total;
+  a.cu_seqlens = cu;
+  a.q_stride = q_stride_tok;
+  a.kv_stride = kv_stride_tok;
+  a.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(static_cast<float>(d));
+  a.window = window;
+  a.sinks = sinks;
+  a.ws = ws;
+  a.status = static_cast<int*>(ws);
+  a.stream = stream;
+  if (cudaMemsetAsync(a.status, 0, sizeof(int), stream) != cudaSuccess) return VS_ERR_CUDA;
+  return launch_attn_tc(a, L) == cudaSuccess ? VS_OK : VS_ERR_CUDA;
+}
+
+vs_status vs_window_attn_fwd(const void* Q, const void* K, const void* V, vs_dtype dtype, int N,
+                             int Hq, int Hkv, int d, int64_t q_stride_tok, int64_t kv_stride_tok,
+                             float softmax_scale, int window, int sinks, void* O, float* lse,
+                             void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return window_impl(Q, K, V, dtype, N, 1, N, nullptr, Hq, Hkv, d, q_stride_tok, kv_stride_tok,
+                     softmax_scale, window, sinks, O, lse, ws, ws_bytes, stream);
+}
+
+vs_status vs_window_attn_fwd_varlen(const void* Q, const void* K, const void* V, vs_dtype dtype,
+                                    int total_tokens, int B, const int32_t* cu_seqlens,
+                                    int max_seqlen, int Hq, int Hkv, int d, int64_t q_stride_tok,
+                                    int64_t kv_stride_tok, float softmax_scale, int window,
+                                    int sinks, void* O, float* lse, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream) {
+  if (!cu_seqlens) return VS_ERR_INVALID_ARG;
+  return window_impl(Q, K, V, dtype, max_seqlen, B, total_tokens, cu_seqlens, Hq, Hkv, d,
+                     q_stride_tok, kv_stride_tok, softmax_scale, window, sinks, O, lse, ws,
+                     ws_bytes, stream);
+}
+
 vs_status vs_read_device_status(const void* ws, cudaStream_t stream, int* flags) {
   if (!ws || !flags) return VS_ERR_INVALID_ARG;
   int v = 0;

@@ -330,9 +330,14 @@ constexpr int kAttnThreads = 320;
 constexpr int kWarpMMA = 8;
 constexpr int kWarpLoad = 9;
 
-enum : int { kModeDense = 0, kModeDenseVS = 1, kModeSplit = 2, kModeBlock = 3 };
-// Kernel instantiations: dense causal, vertical-slash sparse, block sparse.
-enum : int { kAttnDense = 0, kAttnVS = 1, kAttnBlock = 2 };
+enum : int { kModeDense = 0, kModeDenseVS = 1, kModeSplit = 2, kModeBlock = 3, kModeWindow = 4 };
+// Kernel instantiations: dense causal, vertical-slash sparse, block sparse,
+// sliding window with visible first keys.
+enum : int { kAttnDense = 0, kAttnVS = 1, kAttnBlock = 2, kAttnWindow = 3 };
+// Instantiations whose items are kept per sub-tile (Item::flags).
+__host__ __device__ constexpr bool per_sub_items(int mode) {
+  return mode == kAttnBlock || mode == kAttnWindow;
+}
 enum : int { kItemTile = 0, kItemVChunk = 1 };
 
 template <int D>
@@ -365,6 +370,11 @@ struct AttnParams {
   // first, bit 31: for the second)
   const int32_t* bcnt;
   const uint32_t* blist;
+  // sliding window: query i sees key j <= i where i - j < window or j < sinks
+  // (both at most N); V and its token stride for the last key tile
+  int window, sinks;
+  const __nv_bfloat16* V;
+  int64_t kv_stride;
 };
 
 struct UnitInfo {
@@ -420,6 +430,20 @@ __device__ __forceinline__ UnitInfo unit_info(const AttnParams& P, int u) {
     ui.d1start = (int)(hb * P.P * (P.P + 1) + (int64_t)ui.p * (ui.p + 1));
     return ui;
   }
+  if (MODE == kAttnWindow) {
+    // the key blocks of the sinks below the window, then every block from the
+    // first row's window to the diagonal
+    const int lo = max(0, 256 * ui.p - (P.window - 1)) >> 7;
+    ui.mode = kModeWindow;
+    if (256 * ui.p >= ui.Nb) {  // no rows (a shorter sequence of a batch)
+      ui.n = 0;
+      return ui;
+    }
+    ui.nvc = min((P.sinks + 127) >> 7, lo);
+    ui.d1start = lo;
+    ui.n = ui.nvc + last_b - lo + 1;
+    return ui;
+  }
   const int32_t* d1pref = P.pp.d1pref + (int64_t)ui.hs * P.L.d1pref_len;
   // key block b = 2p+1-d' must lie in [0, last_b]  =>  d' in [2p+1-last_b, 2p+1]
   const int lo = 2 * ui.p + 1 - last_b, hi = 2 * ui.p + 1;
@@ -442,10 +466,11 @@ __device__ __forceinline__ UnitInfo unit_info(const AttnParams& P, int u) {
 struct Item {
   int kind;
   int b;      // key block (tile) or chunk index (vertical chunk)
-  int flags;  // block sparse: bit s set iff the block is kept for sub-tile s,
-              // bit 2 + s iff it is the last block kept for sub-tile s
+  int flags;  // block sparse, window: bit s set iff the block is kept for sub-tile
+              // s, bit 2 + s iff it is the last block kept for sub-tile s
 };
 
+template <int MODE>
 __device__ __forceinline__ Item unit_item(const AttnParams& P, const UnitInfo& ui, int k) {
   Item it;
   it.flags = 3;
@@ -454,6 +479,19 @@ __device__ __forceinline__ Item unit_item(const AttnParams& P, const UnitInfo& u
     it.kind = kItemTile;
     it.b = (int)(e & 0xFFFFu);
     it.flags = (int)((e >> 30) | (((e >> 28) & 3u) << 2));
+  } else if (MODE == kAttnWindow) {
+    it.kind = kItemTile;
+    it.b = k < ui.nvc ? k : ui.d1start + (k - ui.nvc);
+    // sub-tile t = 2p + s: rows 128 t .. 128 t + 127 see keys from their first
+    // row's window start to the diagonal block, and the sinks
+    it.flags = 0;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int t = 2 * ui.p + s;
+      const int lo = max(0, 128 * t - (P.window - 1)) >> 7;
+      if (128 * t < ui.Nb && it.b <= t && (it.b >= lo || 128 * it.b < P.sinks))
+        it.flags |= (1 << s) | (it.b == t ? 4 << s : 0);
+    }
   } else if (ui.mode != kModeSplit) {
     it.kind = kItemTile;
     it.b = k;
@@ -501,6 +539,16 @@ __device__ __forceinline__ bool item_mask(const AttnParams& P, const UnitInfo& u
   if (MODE == kAttnBlock && !((it.flags >> (t_sub - 2 * ui.p)) & 1)) {  // (callers skip these)
 #pragma unroll
     for (int q = 0; q < 4; ++q) w[q] = 0u;  // not kept for this sub-tile's query block
+    return true;
+  }
+  if (MODE == kAttnWindow) {
+    const int first = i - P.window + 1;  // of the window
+    if (below && (first <= 128 * b || 128 * b + 128 <= P.sinks)) return false;
+    const int n = below ? 128 : i - 128 * b + 1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = prefix_word(n, 32 * q) &
+             (~prefix_word(first - 128 * b, 32 * q) | prefix_word(P.sinks - 128 * b, 32 * q));
     return true;
   }
   if (MODE != kAttnVS || ui.mode == kModeDense) {
@@ -556,6 +604,21 @@ __device__ __forceinline__ void exp_tile(const uint32_t (&sr)[4][32], float sl2,
     tmem_st16(tS + 16 * q, pk);
   }
   ls = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+}
+
+// One warp writes V rows [0, rows) of a 128-row tile, and zeros below them, in
+// the layout the tile's TMA load gives (64-column halves, 128-byte swizzle).
+template <int D>
+__device__ __forceinline__ void load_v_tail(uint8_t* dst, const __nv_bfloat16* v, int64_t stride,
+                                            int rows, int lane) {
+  constexpr int CH = D / 8;  // 16-byte chunks per row
+#pragma unroll 8
+  for (int e = lane; e < 128 * CH; e += 32) {
+    const int r = e / CH, ch = e % CH;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(v + (int64_t)r * stride + ch * 8));
+    *reinterpret_cast<uint4*>(dst + (ch >> 3) * 16384 + sw128_off(r, ch & 7)) = x;
+  }
 }
 
 template <int D, int MODE>
@@ -618,7 +681,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_after();
   const uint32_t tbase = *tslot;
   const WaitCtx wc{P.wait_limit_ns, P.status, abort_flag};
-  if (MODE == kAttnDense && P.cu && blockIdx.x == 0 && tid == 0) {
+  if ((MODE == kAttnDense || MODE == kAttnWindow) && P.cu && blockIdx.x == 0 && tid == 0) {
     // the sparse path's plan kernel checks the offsets; here the first CTA does
     for (int b = 0; b < P.B; ++b) {
       int64_t t0;
@@ -659,9 +722,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float m_use = -INFINITY, l = 0.f;
       int nproc = 0;  // items this sub-tile has processed
       for (int k = 0; k < ui.n; ++k) {
-        const Item it = unit_item(P, ui, k);
-        // block sparse: the MMA issuer gives this sub-tile only the blocks it keeps
-        if (MODE == kAttnBlock && !((it.flags >> sub) & 1)) continue;
+        const Item it = unit_item<MODE>(P, ui, k);
+        // block sparse, window: the MMA issuer gives this sub-tile only the blocks it keeps
+        if (per_sub_items(MODE) && !((it.flags >> sub) & 1)) continue;
         uint32_t mw[4];
         const bool masked = item_mask<MODE>(P, ui, it, im, t_sub, mw);
         if (!mbar_wait(bar(B_SFULL + sub), scnt & 1, wc)) { ok = false; break; }
@@ -791,15 +854,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const UnitInfo ui = unit_info<MODE>(P, u);
         if (ui.n == 0) continue;
         if (!mbar_wait(bar(B_QFULL), ucount & 1, wc)) { ok = false; break; }
-        if constexpr (MODE == kAttnBlock) {
+        if constexpr (per_sub_items(MODE)) {
           // Each sub-tile gets S and PV only for the blocks it keeps; K and V
           // of every listed block stream through the ring as in the other
           // modes.  At the stage [V(k), K(k+1)]: PV(k) for the sub-tiles
           // keeping block k (O complete after a sub-tile's last one), then
           // S(k+1) for those keeping block k+1 -- after the sub-tile's
           // previous PV in issue order, so S never overwrites an unread P.
-          int fl = unit_item(P, ui, 0).flags;
-          int fl_next = ui.n > 1 ? unit_item(P, ui, 1).flags : 0;
+          int fl = unit_item<MODE>(P, ui, 0).flags;
+          int fl_next = ui.n > 1 ? unit_item<MODE>(P, ui, 1).flags : 0;
           bool started[2] = {false, false};
           uint32_t kslot = seq % S;
           if (!mbar_wait(bar(B_STAGE + stg % S), (stg / S) & 1, wc)) { ok = false; break; }  // [K(0)]
@@ -813,7 +876,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           mma_commit(bar(B_EMPTY + kslot));
           for (int k = 0; k < ui.n && ok; ++k) {
-            const int fl_after = k + 2 < ui.n ? unit_item(P, ui, k + 2).flags : 0;  // early load
+            const int fl_after = k + 2 < ui.n ? unit_item<MODE>(P, ui, k + 2).flags : 0;  // early load
             if (!mbar_wait(bar(B_STAGE + stg % S), (stg / S) & 1, wc)) { ok = false; break; }
             ++stg;
             const uint32_t vslot = seq % S;
@@ -921,7 +984,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int ntiles = 2 * ui.n;
       for (int t = 0; t < ntiles && ok; ++t) {
         const int k = t >> 1, kv = t & 1;
-        const Item it = unit_item(P, ui, k);
+        const Item it = unit_item<MODE>(P, ui, k);
         {
           const uint32_t slot = seq % S;
           if (seq >= (uint32_t)S && !mbar_wait(bar(B_EMPTY + slot), ((seq / S) - 1) & 1, wc)) {
@@ -929,6 +992,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             break;
           }
           const uint32_t fb = bar(B_STAGE + stg % S);
+          if (MODE == kAttnWindow && t == ntiles - 1 && 128 * it.b + 128 > ui.Nb) {
+            // The sequence's last key tile, partly past its end (always a
+            // unit's last tile, alone in its stage).  The rows behind belong
+            // to another sequence or to nobody; their weights are 0, but
+            // 0 * inf or NaN would reach O, so V is written here with zeros
+            // there instead of by TMA.
+            load_v_tail<D>(sKV + slot * C::kTileBytes,
+                           P.V + (tok0 + 128 * it.b) * P.kv_stride + (int64_t)ui.g * D,
+                           P.kv_stride, ui.Nb - 128 * it.b, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fb);
+            ++seq;
+            ++stg;
+            continue;
+          }
           if (t == 0 || kv == 1) {  // first tile of a stage: arm it for all of its bytes
             const int nst = (t == 0 || t == ntiles - 1) ? 1 : 2;
             if (lane == 0) mbar_arrive_expect_tx(fb, nst * C::kTileBytes);
@@ -1039,6 +1118,10 @@ static cudaError_t launch_tc_impl(const AttnArgs& a, const PlanLayout& L) {
   P.pack_vrows = SPARSE ? a.pack_vrows : 0;
   P.bcnt = nullptr;
   P.blist = nullptr;
+  P.window = a.window < a.N ? a.window : a.N;
+  P.sinks = a.sinks < a.N ? a.sinks : a.N;
+  P.V = static_cast<const __nv_bfloat16*>(a.V);
+  P.kv_stride = a.kv_stride;
   if (MODE == kAttnBlock) {
     const BlockPlanLayout B = BlockPlanLayout::make(a.N, a.B * a.Hq);
     P.bcnt = reinterpret_cast<const int32_t*>(static_cast<const char*>(a.ws) + B.off_cnt);
@@ -1057,6 +1140,11 @@ cudaError_t launch_attn_tc(const AttnArgs& a, const PlanLayout& L) {
   if (a.block_mask) {
     if (a.d == 128) return launch_tc_impl<128, kAttnBlock>(a, L);
     if (a.d == 64) return launch_tc_impl<64, kAttnBlock>(a, L);
+    return cudaErrorInvalidValue;
+  }
+  if (a.window > 0) {
+    if (a.d == 128) return launch_tc_impl<128, kAttnWindow>(a, L);
+    if (a.d == 64) return launch_tc_impl<64, kAttnWindow>(a, L);
     return cudaErrorInvalidValue;
   }
   if (a.d == 128)

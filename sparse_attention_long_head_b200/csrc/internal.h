@@ -173,6 +173,7 @@ struct AttnArgs {
   float scale;
   bool sparse;
   const uint32_t* block_mask;  // block sparse: kept key blocks [Hq][T][W] (else null)
+  int window = 0, sinks = 0;   // window > 0: sliding window with the first `sinks` keys visible
   const int32_t* v_idx;
   int64_t v_ld;
   const int32_t* v_cnt;
