@@ -459,6 +459,146 @@ vs_status vs_attn_aggregate_varlen(const void* Q, const void* K, vs_dtype dtype,
                                    void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * The 4-bit paged key/value cache -- where the keys and values of a prefill
+ * go, and the attention of the tokens that follow.  (The summary pages stop at
+ * prefill; these calls continue from what this library computes there: the
+ * column sums of vs_attn_aggregate are the weights that eviction starts from.)
+ *
+ * Pool: `n_pages` pages of vs_kv4_page_bytes(Hkv, d) bytes (device, 16-byte
+ * aligned; d in {64, 128}).  A page holds 64 slots of every KV head; the bytes
+ * of one (page, head) are contiguous, with GR = d / 64:
+ *     key codes   [GR][64 slots][32 bytes]    value codes  likewise
+ *     key pairs   [GR][64 slots] (s, m) bf16  value pairs  likewise
+ * 64 channels (a group) of a slot are eight 32-bit words; bits 4j .. 4j+3 of
+ * word w are the code n of channel 8 w + j, which stands for s n + m.
+ * Table: int32 [B][table_ld] (device); slots [64 i, 64 i + 64) of sequence b
+ * are in page table[b * table_ld + i].  Entries of pages that a call need not
+ * touch are not read and may hold anything.  An entry outside [0, n_pages)
+ * that is touched sets VS_DEVFLAG_BOUNDS; its slots are not written, or count
+ * as invisible.
+ * lens: int32 [B] (device), slots in use, the same for every head of a
+ * sequence.  max_len (host) bounds them: 1 <= max_len <= 2^24, and at most
+ * 64 table_ld.  A length outside [0, max_len] counts as 0 and sets
+ * VS_DEVFLAG_BOUNDS.  B * Hkv <= 65535.
+ * All calls are asynchronous and read lens, table and the other device
+ * arguments when they run, so a captured graph follows their contents.  Calls
+ * on one cache must be ordered by the caller (one stream, or events), and
+ * calls that may overlap need workspaces of their own.
+ */
+#define VS_KV4_PAGE 64
+size_t vs_kv4_page_bytes(int Hkv, int d); /* 0 for an unsupported d */
+
+/*
+ * vs_kv4_append -- quantises new keys and values and writes them behind what
+ * the cache holds: sequence b's new tokens, rows [cu_seqlens[b],
+ * cu_seqlens[b + 1]) of K and V, go to slots [lens[b] - n_b, lens[b]).
+ * Per group of 64 channels x: m = min x, s = bf16((max x - min x) / 15),
+ * n = clamp(rint((x - m) / s), 0, 15) with ties to even, decided exactly;
+ * s = 0 gives n = 0; an infinity or NaN gives a group that reads as NaN.
+ *   K, V     [total_tokens, Hkv, d], VS_BF16 (else VS_ERR_UNSUPPORTED),
+ *            strides as for the attention calls.  Keys carry their rotary
+ *            embedding already: slots have no positions of their own.
+ *   cu_seqlens int32 [B + 1] (device), max_new >= every n_b, as for
+ *            vs_sparse_attn_fwd_varlen; n_b = 0 leaves the sequence alone.
+ *   lens     lengths INCLUDING the new tokens.
+ *   n_tokens int32 [B] (device): tokens seen so far, the new ones included
+ *            (larger than lens after an eviction), or NULL: lens.
+ *   acc, pos fp32 and int32 [B][Hkv][ld] (device), each may be NULL: the
+ *            accumulated attention weight and the position of every slot.
+ *            Entries of the new slots are written: acc[b][g][slot] = sum of
+ *            A_v[h][row] over the query heads h of KV head g (0 without A_v),
+ *            pos[b][g][slot] = n_tokens[b] - n_b + i for the i-th new token.
+ *   A_v      fp32 [Hq][total_tokens] as vs_attn_aggregate_varlen writes it, or
+ *            NULL (needs acc).
+ * A sequence that does not fit (a malformed offset, more new tokens than
+ * lens[b], lens[b] above 64 table_ld or, with acc or pos, above ld) is not
+ * written and sets VS_DEVFLAG_BOUNDS.  ws: 256 bytes, 256-byte aligned.
+ */
+vs_status vs_kv4_append(const void* K, const void* V, vs_dtype dtype, int total_tokens,
+                        const int32_t* cu_seqlens, int max_new, int64_t kv_stride_tok, void* pool,
+                        int n_pages, const int32_t* table, int64_t table_ld, const int32_t* lens,
+                        const int32_t* n_tokens, int B, int max_len, int Hq, int Hkv, int d,
+                        const float* A_v, float* acc, int32_t* pos, int64_t ld, void* ws,
+                        size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * vs_kv4_read -- reads slots [start[b], start[b] + n_b) of every sequence back
+ * as bf16 (s n + m, rounded once), n_b = cu_seqlens[b + 1] - cu_seqlens[b],
+ * into rows [cu_seqlens[b], cu_seqlens[b + 1]) of K and V [total_tokens, Hkv,
+ * d]: a cached prefix for the packed prefill calls.
+ *   start    int32 [B] (device) or NULL: 0.   max_read >= every n_b.
+ * Rows of no sequence are left as they were.  A sequence whose slots do not
+ * all lie in [0, lens[b]) is not written and sets VS_DEVFLAG_BOUNDS, as does a
+ * malformed offset.  ws: 256 bytes, 256-byte aligned.
+ */
+vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64_t table_ld,
+                      const int32_t* lens, const int32_t* start, int B, int max_len, int Hkv, int d,
+                      const int32_t* cu_seqlens, int max_read, int total_tokens, void* K, void* V,
+                      int64_t kv_stride_tok, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * vs_kv4_decode_attn_fwd -- attention of one new token per sequence over its
+ * cached slots (append the token first for it to see itself):
+ *     O[b][h] = sum_t softmax_t(scale q . k_t) v_t over the visible slots t,
+ *     LSE = log sum_t exp(scale q . k_t),   k_t, v_t = s n + m.
+ *   Q        [B, Hq, d], VS_BF16 (else VS_ERR_UNSUPPORTED), row stride
+ *            q_stride_tok; O alike (output).  Hq % Hkv == 0, any ratio.
+ *   window, sinks  window 0 (and sinks 0): every slot t < lens[b].  Else slots
+ *            t >= lens[b] - window and t < sinks, the window attention of the
+ *            prefill at its last row (for caches whose slots are positions:
+ *            after an eviction they are not).  Pages without a visible slot
+ *            are not touched.
+ *   acc_out  fp32 [B][Hkv][ld], or NULL: for t < lens[b]
+ *            acc_out = acc_in + sum over the query heads of the KV head of the
+ *            softmax weight of slot t (0 where it is invisible); acc_in may be
+ *            acc_out itself, or NULL (zeros).  ld >= max_len.  Entries from
+ *            lens[b] on are left as they were.
+ *   lse      fp32 [Hq][B] (output) or NULL.
+ * A sequence without slots gives O = 0 and LSE = -inf.  Results do not depend
+ * on timing: repeated calls give the same bits on the same device.
+ *   ws       vs_kv4_decode_workspace_size(B, Hq, Hkv, d, max_len, acc_out !=
+ *            NULL) bytes, 256-byte aligned (the size depends on the current
+ *            device's SM count; with weights it includes one float per query
+ *            head and slot).
+ * VS_ERR_UNSUPPORTED where the pages of all rows do not fit 32 bits.
+ */
+size_t vs_kv4_decode_workspace_size(int B, int Hq, int Hkv, int d, int max_len, int with_weights);
+vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride_tok,
+                                 const void* pool, int n_pages, const int32_t* table,
+                                 int64_t table_ld, const int32_t* lens, int B, int max_len, int Hq,
+                                 int Hkv, int d, float softmax_scale, int window, int sinks,
+                                 const float* acc_in, float* acc_out, int64_t ld, void* O,
+                                 float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * vs_kv4_evict -- cuts every (sequence, KV head) row to k = min(lens[b], keep)
+ * slots.  What stays, in this order: slots of fixed tokens (pos < sinks or pos
+ * >= n_tokens[b] - recent), then by acc descending (NaN after -inf), ties to
+ * the lower slot.  Slots below k that stay keep their place; the i-th slot
+ * below k that goes is overwritten by the i-th slot at or above k that stays.
+ * Every head keeps its own tokens.
+ *   lens, acc, pos   as vs_kv4_append and vs_kv4_decode_attn_fwd leave them,
+ *            rows of length ld >= max_len; n_tokens as for vs_kv4_append.
+ *   keep, sinks, recent   keep >= 1, sinks >= 0, recent >= 0, sinks + recent
+ *            <= keep.
+ *   lens_out int32 [B], acc_out, pos_out [B][Hkv][ld_out], ld_out >=
+ *            min(keep, max_len): the new lengths, and the kept slots' entries
+ *            ([0, k) of each row).  Not the input buffers.
+ * The pool is changed in place; pages that only held slots at or above k are
+ * free afterwards.  The pages of a sequence that is cut must not be shared
+ * with another sequence.  1 <= max_len <= 2^18.
+ *   ws       vs_kv4_evict_workspace_size(B, Hkv, max_len, keep) bytes,
+ *            256-byte aligned.
+ */
+size_t vs_kv4_evict_workspace_size(int B, int Hkv, int max_len, int keep);
+vs_status vs_kv4_evict(void* pool, int n_pages, const int32_t* table, int64_t table_ld,
+                       const int32_t* lens, const int32_t* n_tokens, int B, int max_len, int Hkv,
+                       int d, const float* acc, const int32_t* pos, int64_t ld, int keep,
+                       int sinks, int recent, int32_t* lens_out, float* acc_out,
+                       int32_t* pos_out, int64_t ld_out, void* ws, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/*
  * Device status of the last call that used `ws`: synchronises `stream`,
  * copies the status word to `*flags` (VS_DEVFLAG_* bits) and returns VS_OK,
  * VS_ERR_DEVICE_TIMEOUT or VS_ERR_DEVICE_BOUNDS accordingly.

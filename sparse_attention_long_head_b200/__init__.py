@@ -48,6 +48,8 @@ EXPORTS = (
     "vs_block_attn_workspace_size_varlen", "vs_block_sparse_attn_fwd_varlen",
     "vs_attn_aggregate_varlen", "vs_select_workspace_size_varlen", "vs_select_varlen",
     "vs_window_attn_fwd", "vs_window_attn_fwd_varlen",
+    "vs_kv4_page_bytes", "vs_kv4_append", "vs_kv4_read", "vs_kv4_decode_workspace_size",
+    "vs_kv4_decode_attn_fwd", "vs_kv4_evict_workspace_size", "vs_kv4_evict",
 )
 
 
@@ -131,6 +133,23 @@ def lib() -> ctypes.CDLL:
         L.vs_window_attn_fwd_varlen.argtypes = [P, P, P, I, I, I, P, I, I, I, I, I64, I64, F, I, I,
                                                 P, P, P, Z, P]
         L.vs_window_attn_fwd_varlen.restype = I
+        L.vs_kv4_page_bytes.argtypes = [I, I]
+        L.vs_kv4_page_bytes.restype = Z
+        L.vs_kv4_append.argtypes = [P, P, I, I, P, I, I64, P, I, P, I64, P, P, I, I, I, I, I, P, P,
+                                    P, I64, P, Z, P]
+        L.vs_kv4_append.restype = I
+        L.vs_kv4_read.argtypes = [P, I, P, I64, P, P, I, I, I, I, P, I, I, P, P, I64, P, Z, P]
+        L.vs_kv4_read.restype = I
+        L.vs_kv4_decode_workspace_size.argtypes = [I, I, I, I, I, I]
+        L.vs_kv4_decode_workspace_size.restype = Z
+        L.vs_kv4_decode_attn_fwd.argtypes = [P, I, I64, P, I, P, I64, P, I, I, I, I, I, F, I, I, P,
+                                             P, I64, P, P, P, Z, P]
+        L.vs_kv4_decode_attn_fwd.restype = I
+        L.vs_kv4_evict_workspace_size.argtypes = [I, I, I, I]
+        L.vs_kv4_evict_workspace_size.restype = Z
+        L.vs_kv4_evict.argtypes = [P, I, P, I64, P, P, I, I, I, I, P, P, I64, I, I, I, P, P, P, I64,
+                                   P, Z, P]
+        L.vs_kv4_evict.restype = I
         L.vs_read_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int)]
         L.vs_read_device_status.restype = I
         L.vs_selftest_wait_timeout.argtypes = [P, U64, P]
@@ -432,6 +451,109 @@ def block_prefill(Q, K, V, alpha, stream=None):
     return O, lse, mask
 
 
+def vs_kv4_page_bytes(Hkv: int, d: int) -> int:
+    return int(lib().vs_kv4_page_bytes(Hkv, d))
+
+
+def vs_kv4_decode_workspace_size(B: int, Hq: int, Hkv: int, d: int, max_len: int,
+                                 with_weights: bool = False) -> int:
+    return int(lib().vs_kv4_decode_workspace_size(B, Hq, Hkv, d, max_len, int(with_weights)))
+
+
+def vs_kv4_evict_workspace_size(B: int, Hkv: int, max_len: int, keep: int) -> int:
+    return int(lib().vs_kv4_evict_workspace_size(B, Hkv, max_len, keep))
+
+
+def _kv4_dims(pool):
+    """(n_pages, Hkv, d) of a pool [n_pages, Hkv, bytes]."""
+    assert pool.dtype == torch.uint8 and pool.dim() == 3 and pool.is_contiguous()
+    n_pages, Hkv, nbytes = pool.shape
+    for d in (64, 128):
+        if vs_kv4_page_bytes(1, d) == nbytes:
+            return n_pages, Hkv, d
+    raise ValueError(f"{nbytes} bytes per page and head are no cache format")
+
+
+def _kv4_max(table, max_len=None):
+    """The bound on lengths that a page table [B, pages] gives, checked against the caller's."""
+    assert table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1
+    room = min(64 * table.shape[1], 1 << 24)
+    if max_len is None:
+        return room
+    if max_len > room:
+        raise ValueError(f"max_len {max_len} is more than the page table holds ({room})")
+    return int(max_len)
+
+
+def _kv4_rows(t):
+    """Row length of an acc or pos tensor [B, Hkv, ld] (its rows may be a slice of longer ones)."""
+    if t is None:
+        return 0
+    assert t.dim() == 3 and (t.shape[2] <= 1 or t.stride(2) == 1)
+    assert t.shape[0] <= 1 or t.stride(0) == t.shape[1] * t.stride(1)
+    return t.stride(1) if t.shape[0] * t.shape[1] > 1 else t.shape[2]
+
+
+def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=None, A_v=None,
+                  acc=None, pos=None, stream=None):
+    """K, V [T, Hkv, d] bf16 of the new tokens; pool uint8 [n_pages, Hkv, bytes]; table int32
+    [B, pages]; lens int32 [B], the new tokens included; acc fp32 and pos int32 [B, Hkv, ld]."""
+    T = K.shape[0]
+    n_pages, Hkv, d = _kv4_dims(pool)
+    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and V.stride(0) == K.stride(0)
+    B = cu_seqlens.numel() - 1
+    ld = _kv4_rows(acc if acc is not None else pos)
+    assert acc is None or pos is None or _kv4_rows(pos) == ld
+    Hq = A_v.shape[0] if A_v is not None else Hkv
+    assert A_v is None or (A_v.shape[1] == T and A_v.is_contiguous())
+    _check(lib().vs_kv4_append(_ptr(K), _ptr(V), _dtype(K), T, _ptr(cu_seqlens), int(max_new),
+                               K.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
+                               _ptr(lens), _ptr(n_tokens), B, _kv4_max(table), Hq, Hkv, d,
+                               _ptr(A_v), _ptr(acc), _ptr(pos), ld, _ptr(ws), ws.numel(),
+                               _stream(stream)), "vs_kv4_append")
+
+
+def vs_kv4_read(pool, table, lens, start, cu_seqlens, max_read, K, V, ws, stream=None):
+    """Slots [start[b], start[b] + n_b) into rows [cu[b], cu[b + 1]) of K, V [T, Hkv, d] bf16;
+    start int32 [B] or None."""
+    n_pages, Hkv, d = _kv4_dims(pool)
+    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and V.stride(0) == K.stride(0)
+    assert K.dtype == V.dtype == torch.bfloat16
+    _check(lib().vs_kv4_read(_ptr(pool), n_pages, _ptr(table), table.stride(0), _ptr(lens),
+                             _ptr(start), cu_seqlens.numel() - 1, _kv4_max(table), Hkv, d,
+                             _ptr(cu_seqlens), int(max_read), K.shape[0], _ptr(K), _ptr(V),
+                             K.stride(0), _ptr(ws), ws.numel(), _stream(stream)), "vs_kv4_read")
+
+
+def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, sinks=0,
+                           acc_in=None, acc_out=None, softmax_scale=0.0, stream=None):
+    """Q, O [B, Hq, d] bf16; lse fp32 [Hq, B] or None; acc_in, acc_out fp32 [B, Hkv, ld] or None."""
+    B, Hq, d = Q.shape
+    n_pages, Hkv, dp = _kv4_dims(pool)
+    assert dp == d and O.shape == Q.shape and O.stride(0) == Q.stride(0)
+    ld = _kv4_rows(acc_out)
+    assert acc_in is None or acc_out is None or _kv4_rows(acc_in) == ld
+    _check(lib().vs_kv4_decode_attn_fwd(
+        _ptr(Q), _dtype(Q), Q.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
+        _ptr(lens), B, _kv4_max(table, max_len), Hq, Hkv, d, float(softmax_scale), int(window),
+        int(sinks), _ptr(acc_in), _ptr(acc_out), ld, _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
+        _stream(stream)), "vs_kv4_decode_attn_fwd")
+
+
+def vs_kv4_evict(pool, table, lens, n_tokens, max_len, acc, pos, keep, sinks, recent, lens_out,
+                 acc_out, pos_out, ws, stream=None):
+    """acc fp32 and pos int32 [B, Hkv, ld]; lens_out int32 [B]; acc_out, pos_out [B, Hkv, ld_out]."""
+    n_pages, Hkv, d = _kv4_dims(pool)
+    B = lens.numel()
+    ld, ld_out = _kv4_rows(acc), _kv4_rows(acc_out)
+    assert _kv4_rows(pos) == ld and _kv4_rows(pos_out) == ld_out
+    _check(lib().vs_kv4_evict(_ptr(pool), n_pages, _ptr(table), table.stride(0), _ptr(lens),
+                              _ptr(n_tokens), B, _kv4_max(table, max_len), Hkv, d, _ptr(acc), _ptr(pos), ld,
+                              int(keep), int(sinks), int(recent), _ptr(lens_out), _ptr(acc_out),
+                              _ptr(pos_out), ld_out, _ptr(ws), ws.numel(), _stream(stream)),
+           "vs_kv4_evict")
+
+
 def vs_read_device_status(ws, stream=None) -> tuple[int, int]:
     """(status code, flags) of the last call that used ``ws`` (synchronises the stream)."""
     flags = ctypes.c_int(0)
@@ -454,6 +576,22 @@ def vs_selftest_exp(x, y, stream=None):
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """A 256-byte aligned uint8 device buffer (torch's allocator aligns to 512)."""
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def kv4_pool(n_pages: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
+    """An uninitialised pool of cache pages, uint8 [n_pages, Hkv, bytes per page and head]."""
+    return torch.empty((n_pages, Hkv, vs_kv4_page_bytes(1, d)), dtype=torch.uint8, device=device)
+
+
+def kv4_decode_attention(Q, pool, table, lens, max_len, window=0, sinks=0, ws=None, stream=None):
+    """Allocates outputs and runs vs_kv4_decode_attn_fwd without weights -> (O, lse [Hq, B])."""
+    B, Hq, d = Q.shape
+    O = torch.empty_like(Q)
+    lse = torch.empty((Hq, B), dtype=torch.float32, device=Q.device)
+    if ws is None:
+        ws = workspace(vs_kv4_decode_workspace_size(B, Hq, pool.shape[1], d, max_len), Q.device)
+    vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window, sinks, stream=stream)
+    return O, lse
 
 
 def select(scores, mode, k_or_cap, tau=1.0, ws=None, stream=None):

@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace vs {
@@ -569,6 +570,181 @@ vs_status vs_window_attn_fwd_varlen(const void* Q, const void* K, const void* V,
   return window_impl(Q, K, V, dtype, max_seqlen, B, total_tokens, cu_seqlens, Hq, Hkv, d,
                      q_stride_tok, kv_stride_tok, softmax_scale, window, sinks, O, lse, ws,
                      ws_bytes, stream);
+}
+
+size_t vs_kv4_page_bytes(int Hkv, int d) {
+  if (Hkv < 1 || (d != 64 && d != 128)) return 0;
+  return (size_t)Hkv * (d / 64) * kKv4GroupBytes;
+}
+
+// The checks every cache call shares; fills the cache's description.
+static vs_status check_cache(const void* pool, int n_pages, const int32_t* table,
+                             int64_t table_ld, const int32_t* lens, int B, int max_len, int Hkv,
+                             int d, const void* ws, Kv4Cache* c) {
+  if (!pool || !table || !lens) return VS_ERR_INVALID_ARG;
+  if (n_pages < 1 || B < 1 || Hkv < 1 || max_len < 1 || table_ld < 1) return VS_ERR_INVALID_ARG;
+  if (table_ld > INT32_MAX || (max_len + 63LL) / 64 > table_ld) return VS_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return VS_ERR_UNSUPPORTED;
+  if (max_len > (1 << 24) || (int64_t)B * Hkv > 65535) return VS_ERR_UNSUPPORTED;
+  if (!aligned(pool, 16)) return VS_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256)) return VS_ERR_WORKSPACE;
+  c->pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  c->n_pages = n_pages;
+  c->table = table;
+  c->table_ld = table_ld;
+  c->lens = lens;
+  c->B = B;
+  c->Hkv = Hkv;
+  c->GR = d / 64;
+  c->max_len = max_len;
+  return VS_OK;
+}
+
+vs_status vs_kv4_append(const void* K, const void* V, vs_dtype dtype, int total_tokens,
+                        const int32_t* cu_seqlens, int max_new, int64_t kv_stride_tok, void* pool,
+                        int n_pages, const int32_t* table, int64_t table_ld, const int32_t* lens,
+                        const int32_t* n_tokens, int B, int max_len, int Hq, int Hkv, int d,
+                        const float* A_v, float* acc, int32_t* pos, int64_t ld, void* ws,
+                        size_t ws_bytes, cudaStream_t stream) {
+  if (!K || !V || !cu_seqlens) return VS_ERR_INVALID_ARG;
+  if (dtype != VS_BF16 && dtype != VS_FP32) return VS_ERR_INVALID_ARG;
+  Kv4AppendArgs a{};
+  const vs_status st =
+      check_cache(pool, n_pages, table, table_ld, lens, B, max_len, Hkv, d, ws, &a.c);
+  if (st != VS_OK) return st;
+  if (total_tokens < 1 || max_new < 1 || Hq < 1 || Hq % Hkv != 0) return VS_ERR_INVALID_ARG;
+  if (kv_stride_tok < (int64_t)Hkv * d) return VS_ERR_INVALID_ARG;
+  if ((A_v && !acc) || ((acc || pos) && ld < 1)) return VS_ERR_INVALID_ARG;
+  if (dtype != VS_BF16 || kv_stride_tok % 8 != 0 || !aligned(K, 16) || !aligned(V, 16))
+    return VS_ERR_UNSUPPORTED;
+  if (ws_bytes < kStatusBytes) return VS_ERR_WORKSPACE;
+  a.K = K;
+  a.V = V;
+  a.kv_stride = kv_stride_tok;
+  a.total = total_tokens;
+  a.cu = cu_seqlens;
+  a.max_new = max_new;
+  a.n_tokens = n_tokens;
+  a.Av = A_v;
+  a.G = Hq / Hkv;
+  a.acc = acc;
+  a.pos = pos;
+  a.ld = ld;
+  a.status = static_cast<int*>(ws);
+  a.stream = stream;
+  if (cudaMemsetAsync(a.status, 0, sizeof(int), stream) != cudaSuccess) return VS_ERR_CUDA;
+  return launch_kv4_append(a) == cudaSuccess ? VS_OK : VS_ERR_CUDA;
+}
+
+vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64_t table_ld,
+                      const int32_t* lens, const int32_t* start, int B, int max_len, int Hkv, int d,
+                      const int32_t* cu_seqlens, int max_read, int total_tokens, void* K, void* V,
+                      int64_t kv_stride_tok, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!K || !V || !cu_seqlens) return VS_ERR_INVALID_ARG;
+  Kv4ReadArgs a{};
+  const vs_status st =
+      check_cache(pool, n_pages, table, table_ld, lens, B, max_len, Hkv, d, ws, &a.c);
+  if (st != VS_OK) return st;
+  if (total_tokens < 1 || max_read < 1 || kv_stride_tok < (int64_t)Hkv * d)
+    return VS_ERR_INVALID_ARG;
+  if (kv_stride_tok % 8 != 0 || !aligned(K, 16) || !aligned(V, 16)) return VS_ERR_UNSUPPORTED;
+  if (ws_bytes < kStatusBytes) return VS_ERR_WORKSPACE;
+  a.start = start;
+  a.cu = cu_seqlens;
+  a.total = total_tokens;
+  a.max_read = max_read;
+  a.K = K;
+  a.V = V;
+  a.kv_stride = kv_stride_tok;
+  a.status = static_cast<int*>(ws);
+  a.stream = stream;
+  if (cudaMemsetAsync(a.status, 0, sizeof(int), stream) != cudaSuccess) return VS_ERR_CUDA;
+  return launch_kv4_read(a) == cudaSuccess ? VS_OK : VS_ERR_CUDA;
+}
+
+size_t vs_kv4_decode_workspace_size(int B, int Hq, int Hkv, int d, int max_len, int with_weights) {
+  if (B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_len < 1)
+    return kStatusBytes;
+  return kv4_decode_ws_bytes(B, Hq, Hkv, d, max_len, with_weights != 0);
+}
+
+vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride_tok,
+                                 const void* pool, int n_pages, const int32_t* table,
+                                 int64_t table_ld, const int32_t* lens, int B, int max_len, int Hq,
+                                 int Hkv, int d, float softmax_scale, int window, int sinks,
+                                 const float* acc_in, float* acc_out, int64_t ld, void* O,
+                                 float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!Q || !O) return VS_ERR_INVALID_ARG;
+  if (dtype != VS_BF16 && dtype != VS_FP32) return VS_ERR_INVALID_ARG;
+  Kv4DecodeArgs a{};
+  const vs_status st =
+      check_cache(pool, n_pages, table, table_ld, lens, B, max_len, Hkv, d, ws, &a.c);
+  if (st != VS_OK) return st;
+  if (Hq < 1 || Hq % Hkv != 0 || q_stride_tok < (int64_t)Hq * d) return VS_ERR_INVALID_ARG;
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return VS_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return VS_ERR_INVALID_ARG;
+  if (acc_in && !acc_out) return VS_ERR_INVALID_ARG;
+  if (acc_out && ld < max_len) return VS_ERR_INVALID_ARG;
+  if (dtype != VS_BF16 || q_stride_tok % 8 != 0 || !aligned(Q, 16)) return VS_ERR_UNSUPPORTED;
+  // pages of all rows are counted in 32 bits
+  const int64_t rows = (int64_t)B * Hkv * ((Hq / Hkv + 7) / 8);
+  if (Hq > (1 << 20) || rows * ((max_len + 63LL) / 64) >= ((int64_t)1 << 31))
+    return VS_ERR_UNSUPPORTED;
+  if (ws_bytes < vs_kv4_decode_workspace_size(B, Hq, Hkv, d, max_len, acc_out != nullptr))
+    return VS_ERR_WORKSPACE;
+  a.Q = Q;
+  a.q_stride = q_stride_tok;
+  a.Hq = Hq;
+  a.G = Hq / Hkv;
+  a.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt(static_cast<float>(d));
+  a.window = window;
+  a.sinks = sinks;
+  a.O = O;
+  a.lse = lse;
+  a.acc_in = acc_in;
+  a.acc_out = acc_out;
+  a.ld = ld;
+  a.ws = ws;
+  a.stream = stream;
+  return launch_kv4_decode(a) == cudaSuccess ? VS_OK : VS_ERR_CUDA;
+}
+
+size_t vs_kv4_evict_workspace_size(int B, int Hkv, int max_len, int keep) {
+  if (B < 1 || Hkv < 1 || max_len < 1 || keep < 1) return kStatusBytes;
+  return kv4_evict_ws_bytes(B, Hkv, max_len, keep);
+}
+
+vs_status vs_kv4_evict(void* pool, int n_pages, const int32_t* table, int64_t table_ld,
+                       const int32_t* lens, const int32_t* n_tokens, int B, int max_len, int Hkv,
+                       int d, const float* acc, const int32_t* pos, int64_t ld, int keep,
+                       int sinks, int recent, int32_t* lens_out, float* acc_out,
+                       int32_t* pos_out, int64_t ld_out, void* ws, size_t ws_bytes,
+                       cudaStream_t stream) {
+  if (!n_tokens || !acc || !pos || !lens_out || !acc_out || !pos_out) return VS_ERR_INVALID_ARG;
+  Kv4EvictArgs a{};
+  const vs_status st =
+      check_cache(pool, n_pages, table, table_ld, lens, B, max_len, Hkv, d, ws, &a.c);
+  if (st != VS_OK) return st;
+  if (lens_out == lens || acc_out == acc || pos_out == pos) return VS_ERR_INVALID_ARG;
+  if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep)
+    return VS_ERR_INVALID_ARG;
+  if (ld < max_len || ld_out < (keep < max_len ? keep : max_len)) return VS_ERR_INVALID_ARG;
+  if (max_len > (1 << 18)) return VS_ERR_UNSUPPORTED;
+  if (ws_bytes < kv4_evict_ws_bytes(B, Hkv, max_len, keep)) return VS_ERR_WORKSPACE;
+  a.n_tokens = n_tokens;
+  a.acc_in = acc;
+  a.pos_in = pos;
+  a.ld_in = ld;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.lens_out = lens_out;
+  a.acc_out = acc_out;
+  a.pos_out = pos_out;
+  a.ld_out = ld_out;
+  a.ws = ws;
+  a.stream = stream;
+  return launch_kv4_evict(a) == cudaSuccess ? VS_OK : VS_ERR_CUDA;
 }
 
 vs_status vs_read_device_status(const void* ws, cudaStream_t stream, int* flags) {

@@ -1,0 +1,732 @@
+// Single-token attention over the 4-bit paged cache (format: kv4.cuh).
+//
+// For query head h of sequence b over the visible slots t of its KV head:
+//     S_t = scale q . k_t,  O = sum_t softmax(S)_t v_t,   k_t, v_t = s n + m
+// per group of 64 channels.  Neither K nor V is ever formed:
+//     q . k = sum_g [ s q.n + m (q.1) ],   O = sum_g [ (p s) . n + (p . m) ],
+// so the codes n go to the tensor cores as they are and s, m multiply scores
+// and weights.  A code becomes bf16 by bit operations alone: 1 + n / 16 is
+// exponent 127 with n in the top four mantissa bits.  The 1 is taken out
+// again in fp32 (by sum q, and by the sum of the bf16 weights, which one MMA
+// with a matrix of ones gives); V is centred on code 8 so that the rounding
+// of p s to bf16 (the only rounding below fp32) acts on n - 8, as it would on
+// the values themselves.
+//
+// Bound by the cache's bytes: 72 per slot, KV head and group (64 codes and
+// pairs of K and V), at G = Hq / Hkv query heads each.  mma.sync m16n8k16 is
+// used, not tcgen05: with 8 or 16 columns of useful work (the query heads of
+// one KV head) the tensor rate is far from the bound, and operands made in
+// registers go straight in, without a trip through shared or tensor memory.
+//
+// One CTA of 12 warps per SM.  All visible pages of all (sequence, KV head)
+// rows form one list, cut into equal ranges, one per CTA; the pages of a
+// range go round the warps.  Each warp streams its pages (one contiguous bulk
+// copy each) through its own ring of two and keeps its own online softmax;
+// the warps of a CTA merge at the end of a row.  A row that several CTAs share
+// leaves one fp32 part per CTA, and the CTA that arrives last joins them in
+// their order, so results do not depend on the timing.  No CTA waits for
+// another.
+#include <cuda_bf16.h>
+
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace vs {
+
+constexpr int kDecWarps = 12;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecStages = 2;
+constexpr int kDecMinPages = kDecWarps;  // per CTA: below, warps would idle beside idle CTAs
+
+// Workspace: status and tickets (zeroed by the call), then parts, the rows'
+// log2-sum-exp and the scores (the last two only where weights are asked for).
+struct DecodeLayout {
+  int HT = 0;       // query heads a row: 8 or 16
+  int HC = 1;       // rows per KV head
+  int Gp = 0;       // scores per slot and KV head (G rounded up to even)
+  int64_t slots = 0;
+  size_t off_tick = 0, off_part = 0, off_lse = 0, off_score = 0, total = 0;
+  size_t part_floats = 0;
+
+  static DecodeLayout make(int B, int Hq, int Hkv, int d, int max_len, bool weights, int sms) {
+    DecodeLayout L;
+    const int G = Hq / Hkv;
+    L.HT = G <= 8 ? 8 : 16;
+    L.HC = (G + L.HT - 1) / L.HT;
+    L.Gp = (G + 1) / 2 * 2;
+    L.slots = (int64_t)ceil_div(max_len, kKv4Page) * kKv4Page;
+    L.part_floats = (size_t)L.HT * (d + 2);
+    L.off_tick = kStatusBytes;
+    L.off_part = align_up(L.off_tick + sizeof(int) * (size_t)B * Hkv * L.HC, 256);
+    L.off_lse = align_up(L.off_part + sizeof(float) * 2 * (size_t)sms * L.part_floats, 256);
+    L.off_score = L.off_lse;
+    L.total = L.off_lse;
+    if (weights) {
+      L.off_score = align_up(L.off_lse + sizeof(float) * (size_t)B * Hq, 256);
+      L.total = L.off_score + sizeof(float) * (size_t)B * Hkv * (size_t)L.slots * L.Gp;
+    }
+    return L;
+  }
+};
+
+struct DecodeParams {
+  Kv4Cache c;
+  const __nv_bfloat16* Q;
+  int64_t q_stride;
+  int Hq, G, HC, Gp;
+  float scale;  // times 16 log2(e): of scores in units of 1 / 16
+  int window, sinks;
+  __nv_bfloat16* O;
+  float* lse;
+  int* status;
+  int* ticket;
+  float* parts;
+  float* lse2;   // [B][Hq] log2-sum-exp, or null
+  float* score;  // [B][Hkv][slots][Gp], or null
+  int64_t slots;
+  uint64_t wait_limit_ns;
+};
+
+// Visible pages of a sequence of n slots: the pages of the first `sinks`
+// slots that lie before the window's, then the window's (or all).
+struct Visible {
+  int first, gap, pages;  // page k of the list is k < first ? k : k + gap
+};
+__device__ __forceinline__ Visible visible_pages(int n, int window, int sinks) {
+  const int np = (n + kKv4Page - 1) / kKv4Page;
+  if (window == 0 || n <= window) return {np, 0, np};
+  const int lo = (n - window) / kKv4Page;
+  const int ns = min((min(sinks, n) + kKv4Page - 1) / kKv4Page, lo);
+  return {ns, lo - ns, ns + np - lo};
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// D += A B, one m16n8k16 bf16 tile.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Nibble j (0..3) of both 16-bit halves as bf16 pairs 1 + n / 16.
+template <int J>
+__device__ __forceinline__ uint32_t codes(uint32_t x) {
+  const uint32_t y = J == 0 ? x << 3 : x >> (J == 0 ? 0 : 4 * J - 3);
+  return (y & 0x00780078u) | 0x3f803f80u;
+}
+
+// Where a CTA's or warp's walk over the list of pages stands.
+struct Cursor {
+  int b, row;  // sequence, and (KV head, head chunk) of it
+  int k;       // page in the row's list
+  Visible v;
+};
+
+__device__ __forceinline__ void cursor_load(const DecodeParams& P, Cursor& q) {
+  int n;
+  kv4_len(P.c, q.b, n);
+  q.v = visible_pages(n, P.window, P.sinks);
+}
+// Moves the cursor on by `by` pages (it stays valid only within the list).
+__device__ __forceinline__ void cursor_add(const DecodeParams& P, Cursor& q, int by) {
+  q.k += by;
+  while (q.k >= q.v.pages) {
+    q.k -= q.v.pages;
+    if (++q.row == P.c.Hkv * P.HC) {
+      q.row = 0;
+      do {
+        if (++q.b >= P.c.B) return;
+        cursor_load(P, q);
+      } while (q.v.pages == 0);
+    }
+  }
+}
+
+template <int GR, int NT>
+__global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const DecodeParams P) {
+  constexpr int D = 64 * GR, HT = 8 * NT;
+  constexpr int kChunk = GR * kKv4GroupBytes;
+  extern __shared__ __align__(128) uint8_t smem[];
+  // ring [warp][stage][kChunk]; a warp's last consumed stage of a row also
+  // carries its part (O [HT][D], m and l [HT]) to the merge
+  static_assert(sizeof(float) * HT * (D + 2) <= kChunk, "a part fits a stage");
+  __shared__ __align__(8) uint64_t bars[kDecWarps * kDecStages];
+  __shared__ int s_abort, s_last;
+  __shared__ int s_sum[kDecThreads];
+  __shared__ int s_start[4];
+  __shared__ const float* s_part[kDecWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const Kv4Cache& c = P.c;
+  const int RPS = c.Hkv * P.HC;  // rows per sequence
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < kDecWarps * kDecStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    fence_mbar_init();
+  }
+  // the list's length, and where this CTA's range starts: thread i sums a
+  // contiguous piece of the sequences
+  const int per = (c.B + kDecThreads - 1) / kDecThreads;
+  const int b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    int n;
+    const bool ok = kv4_len(c, b, n);
+    if (blockIdx.x == 0 && !ok) atomicOr(P.status, VS_DEVFLAG_BOUNDS);
+    mine += visible_pages(n, P.window, P.sinks).pages * RPS;
+  }
+  s_sum[tid] = mine;
+  __syncthreads();
+  for (int o = 1; o < kDecThreads; o <<= 1) {
+    const int x = tid >= o ? s_sum[tid - o] : 0;
+    __syncthreads();
+    s_sum[tid] += x;
+    __syncthreads();
+  }
+  const int total = s_sum[kDecThreads - 1];
+  const int share = max(kDecMinPages, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int f0 = min((int64_t)blockIdx.x * share, (int64_t)total);
+  const int f1 = min((int64_t)f0 + share, (int64_t)total);
+  {
+    int at = s_sum[tid] - mine;
+    if (f0 < f1 && at <= f0 && f0 < at + mine) {
+      int b = b0;
+      for (;; ++b) {
+        int n;
+        kv4_len(c, b, n);
+        const int p = visible_pages(n, P.window, P.sinks).pages * RPS;
+        if (f0 < at + p) break;
+        at += p;
+      }
+      s_start[0] = b;
+      s_start[1] = f0 - at;
+      s_start[2] = at;  // list position of the sequence
+    }
+  }
+  // rows without a visible slot: nobody's range covers them
+  for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+    int n;
+    kv4_len(c, b, n);
+    if (n > 0) continue;
+    for (int e = tid; e < P.Hq * D; e += kDecThreads)
+      P.O[(int64_t)b * P.q_stride + e] = __float2bfloat16_rn(0.f);
+    if (P.lse)
+      for (int h = tid; h < P.Hq; h += kDecThreads) P.lse[(int64_t)h * c.B + b] = -INFINITY;
+  }
+  __syncthreads();
+  if (f0 >= f1) return;
+
+  Cursor seg;  // the CTA's walk, row by row
+  seg.b = s_start[0];
+  cursor_load(P, seg);
+  seg.row = s_start[1] / seg.v.pages;
+  seg.k = s_start[1] % seg.v.pages;
+  Cursor next = seg;  // the next page this warp fetches
+  const int count = f1 - f0;
+  int issued = warp;  // its place in the CTA's range
+  if (issued < count) cursor_add(P, next, warp);
+
+  const WaitCtx wc{P.wait_limit_ns, P.status, &s_abort};
+  uint8_t* ring = smem + warp * kDecStages * kChunk;
+  auto bar = [&](int s) { return smem_u32(&bars[warp * kDecStages + s]); };
+  uint32_t nissue = 0, nwait = 0;  // copies issued and awaited so far
+  uint32_t valid = 0;              // bit s: stage s holds a page of the pool
+  auto issue = [&]() {
+    if (issued >= count) return;
+    const int st = nissue % kDecStages;
+    const int page = next.k < next.v.first ? next.k : next.k + next.v.gap;
+    const uint8_t* src = kv4_page(c, next.b, page, next.row / P.HC);
+    valid = src ? valid | (1u << st) : valid & ~(1u << st);
+    if (lane == 0) {
+      if (src) {
+        mbar_arrive_expect_tx(bar(st), kChunk);
+        bulk_load(smem_u32(ring + st * kChunk), src, kChunk, bar(st));
+      } else {
+        atomicOr(P.status, VS_DEVFLAG_BOUNDS);
+        mbar_arrive(bar(st));
+      }
+    }
+    ++nissue;
+    issued += kDecWarps;
+    if (issued < count) cursor_add(P, next, kDecWarps);
+  };
+  for (int s = 0; s < kDecStages; ++s) issue();
+
+  bool ok = true;
+  for (int at = 0; at < count;) {
+    // ---------------------------------------------- one row, pages [k0, k1)
+    const int k0 = seg.k, k1 = min(seg.v.pages, k0 + (count - at));
+    const int head = seg.row / P.HC, hc = seg.row % P.HC;
+    int n;
+    kv4_len(c, seg.b, n);
+    const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
+    const int heads = min(HT, P.G - hc * HT);
+    const int h0 = head * P.G + hc * HT;  // first query head of the row
+
+    // Q as the B operand of S^T = K Q^T: head gid, channels in the order the
+    // words' nibbles give; and the groups' sums of q for this lane's heads
+    uint32_t qf[NT][GR][2][4];
+    float qs[NT][GR][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int g = 0; g < GR; ++g) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (8 * nt + gid < heads)
+            u = __ldg(reinterpret_cast<const uint4*>(P.Q + (int64_t)seg.b * P.q_stride +
+                                                     (int64_t)(h0 + 8 * nt + gid) * D + 64 * g +
+                                                     8 * (2 * tig + w)));
+          qf[nt][g][w][0] = __byte_perm(u.x, u.z, 0x5410);  // channels 0, 4
+          qf[nt][g][w][1] = __byte_perm(u.x, u.z, 0x7632);  // 1, 5
+          qf[nt][g][w][2] = __byte_perm(u.y, u.w, 0x5410);
+          qf[nt][g][w][3] = __byte_perm(u.y, u.w, 0x7632);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sum += __uint_as_float(qf[nt][g][w][i] << 16) +
+                   __uint_as_float(qf[nt][g][w][i] & 0xffff0000u);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
+        qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
+      }
+    float o[NT][GR][4][4], lw[NT][GR][4];  // O^T tiles; sums of the bf16 weights
+    float m[NT][2], l[NT][2], r[NT][GR][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int g = 0; g < GR; ++g) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          lw[nt][g][x] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nt][g][j][x] = 0.f;
+        }
+        r[nt][g][0] = r[nt][g][1] = 0.f;
+      }
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    int last_stage = -1;
+    // this warp's pages of the row
+    for (int i = at + (warp + kDecWarps - at % kDecWarps) % kDecWarps; i < at + (k1 - k0);
+         i += kDecWarps) {
+      const int k = k0 + (i - at);
+      if (ok && last_stage >= 0) {  // into the stage consumed before this page
+        __syncwarp();
+        issue();
+      }
+      const int st = nwait % kDecStages;
+      if (ok) ok = mbar_wait(bar(st), (nwait / kDecStages) & 1, wc);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {  // a copy may still be on its way into the stage
+        last_stage = -1;
+        continue;
+      }
+      ++nwait;
+      last_stage = st;
+      if (!((valid >> st) & 1)) continue;
+      const uint8_t* pg = ring + st * kChunk;
+      const int page = k < seg.v.first ? k : k + seg.v.gap;
+      const int t0 = page * kKv4Page;
+      // every slot of the page visible?
+      const bool whole = t0 + kKv4Page <= n && (t0 >= lo_slot || t0 + kKv4Page <= P.sinks);
+
+      // row x of a 16-slot tile is slot perm(x): lanes of one load then touch
+      // all banks for both K (rows gid) and V (rows 2 tig, 2 tig + 1)
+      auto perm = [](int x) { return x ^ ((x >> 2) & 1); };
+      float sc[NT][4][4];
+#pragma unroll
+      for (int tl = 0; tl < 4; ++tl) {
+        const int ra = 16 * tl + perm(gid), rb = ra + 8;
+        float cacc[NT][GR][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int g = 0; g < GR; ++g)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) cacc[nt][g][x] = 0.f;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+          const uint2 wa =
+              *reinterpret_cast<const uint2*>(pg + kv4_code_off(GR, 0, g, ra) + 8 * tig);
+          const uint2 wb =
+              *reinterpret_cast<const uint2*>(pg + kv4_code_off(GR, 0, g, rb) + 8 * tig);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t ua = w ? wa.y : wa.x, ub = w ? wb.y : wb.x;
+            const uint32_t a0 = codes<0>(ua), a1 = codes<0>(ub), a2 = codes<1>(ua),
+                           a3 = codes<1>(ub);
+            const uint32_t e0 = codes<2>(ua), e1 = codes<2>(ub), e2 = codes<3>(ua),
+                           e3 = codes<3>(ub);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16(cacc[nt][g], a0, a1, a2, a3, qf[nt][g][w][0], qf[nt][g][w][1]);
+              mma_bf16(cacc[nt][g], e0, e1, e2, e3, qf[nt][g][w][2], qf[nt][g][w][3]);
+            }
+          }
+        }
+        // q.k / 16 = sum_g s (C - sum q) + (m / 16) sum q
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[nt][tl][x] = 0.f;
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+          const uint32_t pa = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 0, g, ra));
+          const uint32_t pb = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 0, g, rb));
+          const float sa = kv4_step(pa), sb = kv4_step(pb);
+          const float ma = fmaf(kv4_min(pa), 0.0625f, -sa), mb = fmaf(kv4_min(pb), 0.0625f, -sb);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              sc[nt][tl][x] = fmaf(x < 2 ? sa : sb, cacc[nt][g][x],
+                                   fmaf(x < 2 ? ma : mb, qs[nt][g][x & 1], sc[nt][tl][x]));
+        }
+        if (!whole) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int t = t0 + (y ? rb : ra);
+            if (t >= n || (t < lo_slot && t >= P.sinks)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                sc[nt][tl][2 * y] = sc[nt][tl][2 * y + 1] = -INFINITY;
+            }
+          }
+        }
+        if (P.score) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int hh = hc * HT + 8 * nt + 2 * tig;
+            if (hh < P.Gp) {
+              float* dst = P.score + (((int64_t)seg.b * c.Hkv + head) * P.slots + t0) * P.Gp + hh;
+              *reinterpret_cast<float2*>(dst + (int64_t)ra * P.Gp) =
+                  make_float2(sc[nt][tl][0], sc[nt][tl][1]);
+              *reinterpret_cast<float2*>(dst + (int64_t)rb * P.Gp) =
+                  make_float2(sc[nt][tl][2], sc[nt][tl][3]);
+            }
+          }
+        }
+      }
+      // online softmax: the page's maximum of this lane's heads
+      float base[NT][2];
+      bool grew = false;
+      float f[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int tl = 0; tl < 4; ++tl) x = fmax3(x, sc[nt][tl][y], sc[nt][tl][y + 2]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x *= P.scale;
+          f[nt][y] = 1.f;
+          if (x > m[nt][y]) {
+            f[nt][y] = ex2_approx(m[nt][y] - x);  // 0 at first
+            m[nt][y] = x;
+            grew = true;
+          }
+          base[nt][y] = m[nt][y] == -INFINITY ? 0.f : m[nt][y];
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            l[nt][y] *= f[nt][y];
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+              r[nt][g][y] *= f[nt][y];
+              lw[nt][g][y] *= f[nt][y];
+              lw[nt][g][y + 2] *= f[nt][y];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                o[nt][g][j][y] *= f[nt][y];
+                o[nt][g][j][y + 2] *= f[nt][y];
+              }
+            }
+          }
+      }
+#pragma unroll
+      for (int tl = 0; tl < 4; ++tl) {
+        const int ra = 16 * tl + perm(gid), rb = ra + 8;
+        float p[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            p[nt][x] = ex2_approx(fmaf(sc[nt][tl][x], P.scale, -base[nt][x & 1]));
+            l[nt][x & 1] += p[nt][x];
+          }
+        const bool dead_a = !whole && (t0 + ra >= n || (t0 + ra < lo_slot && t0 + ra >= P.sinks));
+        const bool dead_b = !whole && (t0 + rb >= n || (t0 + rb < lo_slot && t0 + rb >= P.sinks));
+#pragma unroll
+        for (int g = 0; g < GR; ++g) {
+          uint32_t pa = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 1, g, ra));
+          uint32_t pb = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 1, g, rb));
+          if (dead_a) pa = 0;  // 0 * NaN of a slot never written
+          if (dead_b) pb = 0;
+          const float sa = kv4_step(pa), sb = kv4_step(pb);
+          const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
+          uint32_t bf[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            bf[nt][0] = transpose8(pack_bf16x2(p[nt][0] * sa, p[nt][1] * sa));
+            bf[nt][1] = transpose8(pack_bf16x2(p[nt][2] * sb, p[nt][3] * sb));
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              r[nt][g][y] = fmaf(p[nt][y], ca, fmaf(p[nt][y + 2], cb, r[nt][g][y]));
+            mma_bf16(lw[nt][g], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][0],
+                     bf[nt][1]);
+          }
+          // V^T as the A operand: channel rows of word gid, slots in pairs
+          uint32_t v[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = 16 * tl + perm(2 * tig + (x & 1)) + 8 * (x >> 1);
+            v[x] = *reinterpret_cast<const uint32_t*>(pg + kv4_code_off(GR, 1, g, row) + 4 * gid);
+          }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t x = __byte_perm(v[0], v[1], hf ? 0x7632 : 0x5410);
+            const uint32_t y = __byte_perm(v[2], v[3], hf ? 0x7632 : 0x5410);
+            const uint32_t a0 = codes<0>(x), a1 = codes<1>(x), a2 = codes<0>(y), a3 = codes<1>(y);
+            const uint32_t e0 = codes<2>(x), e1 = codes<3>(x), e2 = codes<2>(y), e3 = codes<3>(y);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16(o[nt][g][2 * hf], a0, a1, a2, a3, bf[nt][0], bf[nt][1]);
+              mma_bf16(o[nt][g][2 * hf + 1], e0, e1, e2, e3, bf[nt][0], bf[nt][1]);
+            }
+          }
+        }
+      }
+    }
+    // ------------------------------------------------------ merge the warps
+    __syncwarp();
+    float* part = nullptr;
+    if (last_stage >= 0) {
+      part = reinterpret_cast<float*>(ring + last_stage * kChunk);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float ls = l[nt][y];
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+          const int h = 8 * nt + 2 * tig + y;
+          if (gid == 0) {
+            part[HT * D + h] = m[nt][y];
+            part[HT * D + HT + h] = ls;
+          }
+#pragma unroll
+          for (int g = 0; g < GR; ++g) {
+            float rs = r[nt][g][y];
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, s);
+            rs = fmaf(-24.f, lw[nt][g][y], rs);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float2*>(part + h * D + 64 * g + 8 * gid + 2 * j) = make_float2(
+                  fmaf(16.f, o[nt][g][j][y], rs), fmaf(16.f, o[nt][g][j][y + 2], rs));
+          }
+        }
+    }
+    if (lane == 0) s_part[warp] = part;
+    __syncthreads();
+    const bool shared = k0 > 0 || k1 < seg.v.pages;
+    const int row_id = seg.b * RPS + seg.row;
+    // a CTA has at most two shared rows: the one its range starts in and the
+    // one it ends in
+    float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * (HT * (D + 2));
+    auto store = [&](int h, int ch, float M, float L, float num) {
+      if (h >= heads) return;
+      const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays
+      P.O[(int64_t)seg.b * P.q_stride + (int64_t)(h0 + h) * D + ch] = __float2bfloat16_rn(num * inv);
+      if (ch == 0) {
+        const float l2 = L > 0.f ? M + log2f(L) : (L == 0.f ? -INFINITY : L);
+        if (P.lse) P.lse[(int64_t)(h0 + h) * c.B + seg.b] = l2 * 0.6931471805599453f;
+        if (P.lse2) P.lse2[(int64_t)seg.b * P.Hq + h0 + h] = l2;
+      }
+    };
+    for (int e = tid; e < HT * D; e += kDecThreads) {
+      const int h = e / D, ch = e % D;
+      float M = -INFINITY, L = 0.f, num = 0.f;
+      for (int w = 0; w < kDecWarps; ++w)
+        if (s_part[w]) M = fmaxf(M, s_part[w][HT * D + h]);
+      const float Mb = M == -INFINITY ? 0.f : M;
+      for (int w = 0; w < kDecWarps; ++w)
+        if (s_part[w]) {
+          const float fw = ex2_approx(s_part[w][HT * D + h] - Mb);
+          L = fmaf(fw, s_part[w][HT * D + HT + h], L);
+          num = fmaf(fw, s_part[w][e], num);
+        }
+      if (!shared) {
+        store(h, ch, M, L, num);
+      } else {
+        out[e] = num;
+        if (ch == 0) {
+          out[HT * D + h] = M;
+          out[HT * D + HT + h] = L;
+        }
+      }
+    }
+    if (shared) {
+      // list positions of the row give the CTAs that share it
+      const int row0 = f0 + at - k0, row1 = row0 + seg.v.pages;
+      const int c0 = row0 / share, c1 = (row1 - 1) / share;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(P.ticket + row_id, 1) == c1 - c0;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        // CTA x's part is its first unless its range starts before the row
+        auto part_of = [&](int x) {
+          return P.parts + (size_t)(2 * x + ((int64_t)x * share < row0 ? 1 : 0)) * (HT * (D + 2));
+        };
+        for (int e = tid; e < HT * D; e += kDecThreads) {
+          const int h = e / D, ch = e % D;
+          float M = -INFINITY, L = 0.f, num = 0.f;
+          for (int x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(part_of(x) + HT * D + h));
+          const float Mb = M == -INFINITY ? 0.f : M;
+          for (int x = c0; x <= c1; ++x) {
+            const float* px = part_of(x);
+            const float fx = ex2_approx(__ldcg(px + HT * D + h) - Mb);
+            L = fmaf(fx, __ldcg(px + HT * D + HT + h), L);
+            num = fmaf(fx, __ldcg(px + e), num);
+          }
+          store(h, ch, M, L, num);
+        }
+      }
+    }
+    __syncthreads();  // the parts in the ring are read
+    if (last_stage >= 0) {
+      fence_proxy_async_smem();  // generic accesses of the stage before its next copy
+      __syncwarp();
+      issue();
+    }
+    at += k1 - k0;
+    if (at < count) cursor_add(P, seg, k1 - k0);
+  }
+  // copies not awaited (only after a wait gave up) land before shared memory is released
+  if (lane == 0)
+    for (; nwait < nissue; ++nwait)
+      mbar_wait_drain(bar(nwait % kDecStages), (nwait / kDecStages) & 1, P.wait_limit_ns);
+}
+
+// acc_out = acc_in + sum over the KV head's query heads of the softmax weight,
+// per slot; invisible slots keep their sum.
+__global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const float* acc_in,
+                                                          float* acc_out, int64_t ld) {
+  const Kv4Cache& c = P.c;
+  const int b = blockIdx.y / c.Hkv, head = blockIdx.y % c.Hkv;
+  int n;
+  kv4_len(c, b, n);
+  const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
+  const float* lse2 = P.lse2 + (int64_t)b * P.Hq + (int64_t)head * P.G;
+  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
+    const int64_t at = ((int64_t)b * c.Hkv + head) * ld + t;
+    float sum = acc_in ? acc_in[at] : 0.f;
+    if ((t >= lo_slot || t < P.sinks) && kv4_page(c, b, t >> 6, head)) {
+      const float* s = P.score + (((int64_t)b * c.Hkv + head) * P.slots + t) * P.Gp;
+      float w = 0.f;
+      for (int h = 0; h < P.G; h += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(s + h);
+        w += ex2_approx(fmaf(x.x, P.scale, -__ldg(lse2 + h)));
+        if (h + 1 < P.G) w += ex2_approx(fmaf(x.y, P.scale, -__ldg(lse2 + h + 1)));
+      }
+      sum += w;
+    }
+    acc_out[at] = sum;
+  }
+}
+
+size_t kv4_decode_ws_bytes(int B, int Hq, int Hkv, int d, int max_len, bool weights) {
+  return DecodeLayout::make(B, Hq, Hkv, d, max_len, weights, device_sm_count()).total;
+}
+
+template <int GR, int NT>
+static cudaError_t launch_decode_impl(const DecodeParams& P, int grid, cudaStream_t stream) {
+  auto kern = kv4_decode_kernel<GR, NT>;
+  constexpr int smem = kDecWarps * kDecStages * GR * kKv4GroupBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kDecThreads, smem, stream>>>(P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
+  const int sms = device_sm_count(), d = a.c.GR * 64;
+  const DecodeLayout L =
+      DecodeLayout::make(a.c.B, a.Hq, a.c.Hkv, d, a.c.max_len, a.acc_out != nullptr, sms);
+  char* ws = static_cast<char*>(a.ws);
+  // status word and tickets
+  cudaError_t e = cudaMemsetAsync(ws, 0, L.off_part, a.stream);
+  if (e != cudaSuccess) return e;
+  DecodeParams P;
+  P.c = a.c;
+  P.Q = static_cast<const __nv_bfloat16*>(a.Q);
+  P.q_stride = a.q_stride;
+  P.Hq = a.Hq;
+  P.G = a.G;
+  P.HC = L.HC;
+  P.Gp = L.Gp;
+  P.scale = a.scale * (16.f * 1.4426950408889634f);
+  P.window = a.window;
+  P.sinks = a.sinks;
+  P.O = static_cast<__nv_bfloat16*>(a.O);
+  P.lse = a.lse;
+  P.status = reinterpret_cast<int*>(ws);
+  P.ticket = reinterpret_cast<int*>(ws + L.off_tick);
+  P.parts = reinterpret_cast<float*>(ws + L.off_part);
+  P.lse2 = a.acc_out ? reinterpret_cast<float*>(ws + L.off_lse) : nullptr;
+  P.score = a.acc_out ? reinterpret_cast<float*>(ws + L.off_score) : nullptr;
+  P.slots = L.slots;
+  P.wait_limit_ns = kDefaultWaitLimitNs;
+  const int64_t rows = (int64_t)a.c.B * a.c.Hkv * L.HC;
+  // no more CTAs than the longest possible list fills
+  const int64_t most = rows * (L.slots / kKv4Page);
+  const int64_t want = (most + kDecMinPages - 1) / kDecMinPages;
+  const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
+  if (L.HT == 8)
+    e = a.c.GR == 1 ? launch_decode_impl<1, 1>(P, grid, a.stream)
+                    : launch_decode_impl<2, 1>(P, grid, a.stream);
+  else
+    e = a.c.GR == 1 ? launch_decode_impl<1, 2>(P, grid, a.stream)
+                    : launch_decode_impl<2, 2>(P, grid, a.stream);
+  if (e != cudaSuccess || !a.acc_out) return e;
+  const int64_t per_row = (L.slots + 255) / 256;
+  const int64_t cap = ceil_div(16LL * sms, a.c.B * a.c.Hkv);
+  const int gx = (int)(per_row < cap ? per_row : cap);
+  kv4_weights_kernel<<<dim3(gx < 1 ? 1 : gx, a.c.B * a.c.Hkv), 256, 0, a.stream>>>(P, a.acc_in,
+                                                                                  a.acc_out, a.ld);
+  return cudaGetLastError();
+}
+
+}  // namespace vs
