@@ -554,6 +554,8 @@ vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64
  *            acc_out itself, or NULL (zeros).  ld >= max_len.  Entries from
  *            lens[b] on are left as they were.
  *   lse      fp32 [Hq][B] (output) or NULL.
+ * The values' steps s are expected in [2^-40, 2^60] and |Q| below 2^113; beyond
+ * that results lose precision or overflow.
  * A sequence without slots gives O = 0 and LSE = -inf.  Results do not depend
  * on timing: repeated calls give the same bits on the same device.
  *   ws       vs_kv4_decode_workspace_size(B, Hq, Hkv, d, max_len, acc_out !=

@@ -685,7 +685,8 @@ vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride
   if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return VS_ERR_INVALID_ARG;
   if (acc_in && !acc_out) return VS_ERR_INVALID_ARG;
   if (acc_out && ld < max_len) return VS_ERR_INVALID_ARG;
-  if (dtype != VS_BF16 || q_stride_tok % 8 != 0 || !aligned(Q, 16)) return VS_ERR_UNSUPPORTED;
+  if (dtype != VS_BF16 || q_stride_tok % 8 != 0 || !aligned(Q, 16) || !aligned(O, 16))
+    return VS_ERR_UNSUPPORTED;
   // pages of all rows are counted in 32 bits
   const int64_t rows = (int64_t)B * Hkv * ((Hq / Hkv + 7) / 8);
   if (Hq > (1 << 20) || rows * ((max_len + 63LL) / 64) >= ((int64_t)1 << 31))

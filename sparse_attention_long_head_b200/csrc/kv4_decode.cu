@@ -5,12 +5,17 @@
 // per group of 64 channels.  Neither K nor V is ever formed:
 //     q . k = sum_g [ s q.n + m (q.1) ],   O = sum_g [ (p s) . n + (p . m) ],
 // so the codes n go to the tensor cores as they are and s, m multiply scores
-// and weights.  A code becomes bf16 by bit operations alone: 1 + n / 16 is
-// exponent 127 with n in the top four mantissa bits.  The 1 is taken out
-// again in fp32 (by sum q, and by the sum of the bf16 weights, which one MMA
-// with a matrix of ones gives); V is centred on code 8 so that the rounding
-// of p s to bf16 (the only rounding below fp32) acts on n - 8, as it would on
-// the values themselves.
+// and weights.  A code needs no conversion: the bits of an integer below 256
+// are a bf16 too, n 2^-133 (subnormal below 128; the first normal binade
+// continues the same line), which the tensor cores multiply exactly.  A word
+// therefore gives its eight codes by four ANDs and one shift: bits 0..3 are n,
+// bits 4..7 are 16 n.  The other operand makes up for the 2^-133: q is scaled
+// by a power of two per head (max |q| to 2^118) and the weights carry 2^48
+// throughout (in the exponential's argument, so that O and l share it).  The
+// 16 of odd codes goes into q, and for V into the row's final factor.
+// V is centred on code 8 (a second MMA with the constant -8 per V tile), so
+// that the rounding of p s to bf16, the only rounding below fp32, acts on
+// n - 8, as it would on the values themselves, and the running sums stay small.
 //
 // Bound by the cache's bytes: 72 per slot, KV head and group (64 codes and
 // pairs of K and V), at G = Hq / Hkv query heads each.  mma.sync m16n8k16 is
@@ -36,6 +41,9 @@ namespace vs {
 constexpr int kDecWarps = 12;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecStages = 2;
+// The weights carry 2^kShift: V steps s from 2^-40 (below, the products with
+// codes of 2^-133 lose bits) to 2^60 (above, sums over long rows overflow).
+constexpr float kShift = 48.f;
 constexpr int kDecMinPages = kDecWarps;  // per CTA: below, warps would idle beside idle CTAs
 
 // Workspace: status and tickets (zeroed by the call), then parts, the rows'
@@ -74,7 +82,7 @@ struct DecodeParams {
   const __nv_bfloat16* Q;
   int64_t q_stride;
   int Hq, G, HC, Gp;
-  float scale;  // times 16 log2(e): of scores in units of 1 / 16
+  float scale;  // times log2(e)
   int window, sinks;
   __nv_bfloat16* O;
   float* lse;
@@ -82,7 +90,7 @@ struct DecodeParams {
   int* ticket;
   float* parts;
   float* lse2;   // [B][Hq] log2-sum-exp, or null
-  float* score;  // [B][Hkv][slots][Gp], or null
+  float* score;  // [B][Hkv][slots][Gp] scores times scale, or null
   int64_t slots;
   uint64_t wait_limit_ns;
 };
@@ -126,11 +134,34 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Nibble j (0..3) of both 16-bit halves as bf16 pairs 1 + n / 16.
-template <int J>
-__device__ __forceinline__ uint32_t codes(uint32_t x) {
-  const uint32_t y = J == 0 ? x << 3 : x >> (J == 0 ? 0 : 4 * J - 3);
-  return (y & 0x00780078u) | 0x3f803f80u;
+// The same with nothing added: D = A B.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Codes at bits 0..3 and at bits 4..7 of both 16-bit halves, as bf16 pairs
+// n 2^-133 and 16 n 2^-133.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return x & 0x000f000fu; }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t x) { return x & 0x00f000f0u; }
+constexpr uint32_t kMinus8 = 0x80088008u;    // -8 2^-133 twice
+constexpr uint32_t kMinus128 = 0x80808080u;  // -128 2^-133 twice
+
+// 2^(field - 127) as a float, field in [1, 254].
+__device__ __forceinline__ float pow2_field(int field) {
+  return __uint_as_float((uint32_t)field << 23);
+}
+
+__device__ __forceinline__ void axpy(float4& y, float a, const float4& x) {
+  y.x = fmaf(a, x.x, y.x);
+  y.y = fmaf(a, x.y, y.y);
+  y.z = fmaf(a, x.z, y.z);
+  y.w = fmaf(a, x.w, y.w);
 }
 
 // Where a CTA's or warp's walk over the list of pages stands.
@@ -170,9 +201,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
   static_assert(sizeof(float) * HT * (D + 2) <= kChunk, "a part fits a stage");
   __shared__ __align__(8) uint64_t bars[kDecWarps * kDecStages];
   __shared__ int s_abort, s_last;
-  __shared__ int s_sum[kDecThreads];
-  __shared__ int s_start[4];
+  __shared__ int s_sum[kDecWarps];
+  __shared__ int s_start[2];
   __shared__ const float* s_part[kDecWarps];
+  __shared__ float s_fac[kDecWarps][HT], s_sumw[kDecWarps][HT], s_join[2 * HT], s_inv[HT];
+  constexpr int kJoin = (HT * D + 4 * kDecThreads - 1) / (4 * kDecThreads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const Kv4Cache& c = P.c;
@@ -194,20 +227,25 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
     if (blockIdx.x == 0 && !ok) atomicOr(P.status, VS_DEVFLAG_BOUNDS);
     mine += visible_pages(n, P.window, P.sinks).pages * RPS;
   }
-  s_sum[tid] = mine;
-  __syncthreads();
-  for (int o = 1; o < kDecThreads; o <<= 1) {
-    const int x = tid >= o ? s_sum[tid - o] : 0;
-    __syncthreads();
-    s_sum[tid] += x;
-    __syncthreads();
+  int incl = mine;  // over the lanes, then over the warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
   }
-  const int total = s_sum[kDecThreads - 1];
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
   const int share = max(kDecMinPages, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   const int f0 = min((int64_t)blockIdx.x * share, (int64_t)total);
   const int f1 = min((int64_t)f0 + share, (int64_t)total);
   {
-    int at = s_sum[tid] - mine;
+    int at = before;
     if (f0 < f1 && at <= f0 && f0 < at + mine) {
       int b = b0;
       for (;; ++b) {
@@ -219,7 +257,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       }
       s_start[0] = b;
       s_start[1] = f0 - at;
-      s_start[2] = at;  // list position of the sequence
     }
   }
   // rows without a visible slot: nobody's range covers them
@@ -283,14 +320,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
     const int h0 = head * P.G + hc * HT;  // first query head of the row
 
     // Q as the B operand of S^T = K Q^T: head gid, channels in the order the
-    // words' nibbles give; and the groups' sums of q for this lane's heads
+    // words' codes give, scaled by f = 2^(field - 127), odd codes' by f / 16.
+    // For this lane's heads: the groups' sums of q, in the units f 2^-133 of
+    // the scores, and what takes scores from these units to base 2.
     uint32_t qf[NT][GR][2][4];
-    float qs[NT][GR][2];
+    float qs[NT][GR][2], sl[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t big = 0;
 #pragma unroll
-      for (int g = 0; g < GR; ++g) {
-        float sum = 0.f;
+      for (int g = 0; g < GR; ++g)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           uint4 u = make_uint4(0, 0, 0, 0);
@@ -302,32 +341,54 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
           qf[nt][g][w][1] = __byte_perm(u.x, u.z, 0x7632);  // 1, 5
           qf[nt][g][w][2] = __byte_perm(u.y, u.w, 0x5410);
           qf[nt][g][w][3] = __byte_perm(u.y, u.w, 0x7632);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sum += __uint_as_float(qf[nt][g][w][i] << 16) +
-                   __uint_as_float(qf[nt][g][w][i] & 0xffff0000u);
+          // largest exponent, as the bits of |q|
+          const uint32_t x = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                      __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+          big = max(big, max(x & 0xffffu, x >> 16));
         }
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // max |q| f in [2^118, 2^119); f at most 2^127, and at least 2^6 (for |q|
+      // from 2^113 on), where the scale of the scores ends
+      const int field = min(254, max(133, 372 - (int)(big >> 7)));
+      const float f = pow2_field(field);
+#pragma unroll
+      for (int g = 0; g < GR; ++g) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = __uint_as_float(qf[nt][g][w][i] << 16) * f;
+            const float b = __uint_as_float(qf[nt][g][w][i] & 0xffff0000u) * f;
+            sum += a + b;
+            qf[nt][g][w][i] =
+                i & 1 ? pack_bf16x2(a * 0.0625f, b * 0.0625f) : pack_bf16x2(a, b);
+          }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
-        qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
+        sum *= 0x1p-100f;
+        qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * tig) * 0x1p-33f;
+        qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4) * 0x1p-33f;
       }
-    float o[NT][GR][4][4], lw[NT][GR][4];  // O^T tiles; sums of the bf16 weights
-    float m[NT][2], l[NT][2], r[NT][GR][2];
+      const float back = P.scale * pow2_field(387 - field);  // scale 2^133 / f
+      sl[nt][0] = __shfl_sync(0xffffffffu, back, 8 * tig);
+      sl[nt][1] = __shfl_sync(0xffffffffu, back, 8 * tig + 4);
+    }
+    float o[NT][GR][4][4];  // O^T tiles, centred on code 8, in units of 2^-133
+    float m[NT][2], nb[NT][2], l[NT][2], r[NT][GR][2];  // p = 2^(score sl + nb)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int g = 0; g < GR; ++g) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          lw[nt][g][x] = 0.f;
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[nt][g][j][x] = 0.f;
-        }
         r[nt][g][0] = r[nt][g][1] = 0.f;
       }
       m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = nb[nt][0] = nb[nt][1] = 0.f;
     }
     int last_stage = -1;
     // this warp's pages of the row
@@ -354,67 +415,56 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       // every slot of the page visible?
       const bool whole = t0 + kKv4Page <= n && (t0 >= lo_slot || t0 + kKv4Page <= P.sinks);
 
-      // row x of a 16-slot tile is slot perm(x): lanes of one load then touch
-      // all banks for both K (rows gid) and V (rows 2 tig, 2 tig + 1)
+      auto hidden = [&](int t) { return t >= n || (t < lo_slot && t >= P.sinks); };
+
+      // Tiles of 16 slots; row x of a tile is its slot perm(x), so that the
+      // lanes of one load touch all banks for both K (rows gid) and V (rows
+      // 2 tig, 2 tig + 1).  One tile's code, looped: a short row runs it from
+      // a cold instruction cache.
       auto perm = [](int x) { return x ^ ((x >> 2) & 1); };
-      float sc[NT][4][4];
-#pragma unroll
-      for (int tl = 0; tl < 4; ++tl) {
-        const int ra = 16 * tl + perm(gid), rb = ra + 8;
-        float cacc[NT][GR][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int g = 0; g < GR; ++g)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) cacc[nt][g][x] = 0.f;
+      const int ra = perm(gid);
+      const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, ra) + 8 * tig;
+      const uint8_t* va = pg + kv4_code_off(GR, 1, 0, perm(2 * tig)) + 4 * gid;
+      const uint8_t* vb = pg + kv4_code_off(GR, 1, 0, perm(2 * tig + 1)) + 4 * gid;
+      const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, ra);
+      const int tiles = min(4, (n - t0 + 15) / 16);
+#pragma unroll 1
+      for (int tl = 0; tl < tiles; ++tl, kc += 512, va += 512, vb += 512, pr += 64) {
+        float sc[NT][4];
 #pragma unroll
         for (int g = 0; g < GR; ++g) {
-          const uint2 wa =
-              *reinterpret_cast<const uint2*>(pg + kv4_code_off(GR, 0, g, ra) + 8 * tig);
-          const uint2 wb =
-              *reinterpret_cast<const uint2*>(pg + kv4_code_off(GR, 0, g, rb) + 8 * tig);
+          const uint2 wa = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes);
+          const uint2 wb = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes + 256);
+          const uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs);
+          const uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 32);
+          const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
+          const float sa = kv4_step(pa), sb = kv4_step(pb);
+          const float ma = kv4_min(pa), mb = kv4_min(pb);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t ua = w ? wa.y : wa.x, ub = w ? wb.y : wb.x;
-            const uint32_t a0 = codes<0>(ua), a1 = codes<0>(ub), a2 = codes<1>(ua),
-                           a3 = codes<1>(ub);
-            const uint32_t e0 = codes<2>(ua), e1 = codes<2>(ub), e2 = codes<3>(ua),
-                           e3 = codes<3>(ub);
+          for (int nt = 0; nt < NT; ++nt) {
+            float cacc[4];
+            mma_bf16_first(cacc, codes_lo(wa.x), codes_lo(wb.x), codes_hi(wa.x), codes_hi(wb.x),
+                           qf[nt][g][0][0], qf[nt][g][0][1]);
+            mma_bf16(cacc, codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb),
+                     qf[nt][g][0][2], qf[nt][g][0][3]);
+            mma_bf16(cacc, codes_lo(wa.y), codes_lo(wb.y), codes_hi(wa.y), codes_hi(wb.y),
+                     qf[nt][g][1][0], qf[nt][g][1][1]);
+            mma_bf16(cacc, codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb),
+                     qf[nt][g][1][2], qf[nt][g][1][3]);
+            // q.k = sum_g s (q.n) + m (q.1)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(cacc[nt][g], a0, a1, a2, a3, qf[nt][g][w][0], qf[nt][g][w][1]);
-              mma_bf16(cacc[nt][g], e0, e1, e2, e3, qf[nt][g][w][2], qf[nt][g][w][3]);
+            for (int x = 0; x < 4; ++x) {
+              const float mm = x < 2 ? ma : mb, ss = x < 2 ? sa : sb, qq = qs[nt][g][x & 1];
+              sc[nt][x] = fmaf(ss, cacc[x], g == 0 ? mm * qq : fmaf(mm, qq, sc[nt][x]));
             }
           }
         }
-        // q.k / 16 = sum_g s (C - sum q) + (m / 16) sum q
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[nt][tl][x] = 0.f;
-#pragma unroll
-        for (int g = 0; g < GR; ++g) {
-          const uint32_t pa = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 0, g, ra));
-          const uint32_t pb = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 0, g, rb));
-          const float sa = kv4_step(pa), sb = kv4_step(pb);
-          const float ma = fmaf(kv4_min(pa), 0.0625f, -sa), mb = fmaf(kv4_min(pb), 0.0625f, -sb);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              sc[nt][tl][x] = fmaf(x < 2 ? sa : sb, cacc[nt][g][x],
-                                   fmaf(x < 2 ? ma : mb, qs[nt][g][x & 1], sc[nt][tl][x]));
-        }
+        const int ta = t0 + 16 * tl + ra, tb = ta + 8;
         if (!whole) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int t = t0 + (y ? rb : ra);
-            if (t >= n || (t < lo_slot && t >= P.sinks)) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                sc[nt][tl][2 * y] = sc[nt][tl][2 * y + 1] = -INFINITY;
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            if (hidden(ta)) sc[nt][0] = sc[nt][1] = -INFINITY;
+            if (hidden(tb)) sc[nt][2] = sc[nt][3] = -INFINITY;
           }
         }
         if (P.score) {
@@ -422,76 +472,68 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
           for (int nt = 0; nt < NT; ++nt) {
             const int hh = hc * HT + 8 * nt + 2 * tig;
             if (hh < P.Gp) {
-              float* dst = P.score + (((int64_t)seg.b * c.Hkv + head) * P.slots + t0) * P.Gp + hh;
-              *reinterpret_cast<float2*>(dst + (int64_t)ra * P.Gp) =
-                  make_float2(sc[nt][tl][0], sc[nt][tl][1]);
-              *reinterpret_cast<float2*>(dst + (int64_t)rb * P.Gp) =
-                  make_float2(sc[nt][tl][2], sc[nt][tl][3]);
+              float* dst = P.score + (((int64_t)seg.b * c.Hkv + head) * P.slots + ta) * P.Gp + hh;
+              *reinterpret_cast<float2*>(dst) =
+                  make_float2(sc[nt][0] * sl[nt][0], sc[nt][1] * sl[nt][1]);
+              *reinterpret_cast<float2*>(dst + 8 * P.Gp) =
+                  make_float2(sc[nt][2] * sl[nt][0], sc[nt][3] * sl[nt][1]);
             }
           }
         }
-      }
-      // online softmax: the page's maximum of this lane's heads
-      float base[NT][2];
-      bool grew = false;
-      float f[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float x = -INFINITY;
-#pragma unroll
-          for (int tl = 0; tl < 4; ++tl) x = fmax3(x, sc[nt][tl][y], sc[nt][tl][y + 2]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x *= P.scale;
-          f[nt][y] = 1.f;
-          if (x > m[nt][y]) {
-            f[nt][y] = ex2_approx(m[nt][y] - x);  // 0 at first
-            m[nt][y] = x;
-            grew = true;
-          }
-          base[nt][y] = m[nt][y] == -INFINITY ? 0.f : m[nt][y];
-        }
-      if (__any_sync(0xffffffffu, grew)) {
+        // Online softmax.  The running maximum follows only when a score
+        // passes it by 2^8: the weights have room, and the lanes' maxima need
+        // not be joined for every tile.
+        bool need = false;
+        float mx[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            l[nt][y] *= f[nt][y];
+            mx[nt][y] = fmaxf(sc[nt][y], sc[nt][y + 2]) * sl[nt][y];
+            need |= mx[nt][y] > m[nt][y] + 8.f;
+          }
+        if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-            for (int g = 0; g < GR; ++g) {
-              r[nt][g][y] *= f[nt][y];
-              lw[nt][g][y] *= f[nt][y];
-              lw[nt][g][y + 2] *= f[nt][y];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                o[nt][g][j][y] *= f[nt][y];
-                o[nt][g][j][y + 2] *= f[nt][y];
+            for (int y = 0; y < 2; ++y) {
+              float x = mx[nt][y];
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              if (x > m[nt][y]) {
+                const float f = ex2_approx(m[nt][y] - x);  // 0 at first
+                m[nt][y] = x;
+                nb[nt][y] = kShift - x;
+                l[nt][y] *= f;
+#pragma unroll
+                for (int g = 0; g < GR; ++g) {
+                  r[nt][g][y] *= f;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    o[nt][g][j][y] *= f;
+                    o[nt][g][j][y + 2] *= f;
+                  }
+                }
               }
             }
-          }
-      }
-#pragma unroll
-      for (int tl = 0; tl < 4; ++tl) {
-        const int ra = 16 * tl + perm(gid), rb = ra + 8;
+        }
         float p[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            p[nt][x] = ex2_approx(fmaf(sc[nt][tl][x], P.scale, -base[nt][x & 1]));
+            p[nt][x] = ex2_approx(fmaf(sc[nt][x], sl[nt][x & 1], nb[nt][x & 1]));
             l[nt][x & 1] += p[nt][x];
           }
-        const bool dead_a = !whole && (t0 + ra >= n || (t0 + ra < lo_slot && t0 + ra >= P.sinks));
-        const bool dead_b = !whole && (t0 + rb >= n || (t0 + rb < lo_slot && t0 + rb >= P.sinks));
 #pragma unroll
         for (int g = 0; g < GR; ++g) {
-          uint32_t pa = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 1, g, ra));
-          uint32_t pb = *reinterpret_cast<const uint32_t*>(pg + kv4_pair_off(GR, 1, g, rb));
-          if (dead_a) pa = 0;  // 0 * NaN of a slot never written
-          if (dead_b) pb = 0;
+          uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs);
+          uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 32);
+          if (!whole) {  // 0 * NaN of a slot never written
+            if (hidden(ta)) pa = 0;
+            if (hidden(tb)) pb = 0;
+          }
           const float sa = kv4_step(pa), sb = kv4_step(pb);
           const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
           uint32_t bf[NT][2];
@@ -502,32 +544,47 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
 #pragma unroll
             for (int y = 0; y < 2; ++y)
               r[nt][g][y] = fmaf(p[nt][y], ca, fmaf(p[nt][y + 2], cb, r[nt][g][y]));
-            mma_bf16(lw[nt][g], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, bf[nt][0],
-                     bf[nt][1]);
           }
           // V^T as the A operand: channel rows of word gid, slots in pairs
-          uint32_t v[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = 16 * tl + perm(2 * tig + (x & 1)) + 8 * (x >> 1);
-            v[x] = *reinterpret_cast<const uint32_t*>(pg + kv4_code_off(GR, 1, g, row) + 4 * gid);
-          }
+          const uint32_t v0 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes);
+          const uint32_t v1 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes);
+          const uint32_t v2 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes + 256);
+          const uint32_t v3 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes + 256);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t x = __byte_perm(v[0], v[1], hf ? 0x7632 : 0x5410);
-            const uint32_t y = __byte_perm(v[2], v[3], hf ? 0x7632 : 0x5410);
-            const uint32_t a0 = codes<0>(x), a1 = codes<1>(x), a2 = codes<0>(y), a3 = codes<1>(y);
-            const uint32_t e0 = codes<2>(x), e1 = codes<3>(x), e2 = codes<2>(y), e3 = codes<3>(y);
+            const uint32_t x = __byte_perm(v0, v1, hf ? 0x7632 : 0x5410);
+            const uint32_t y = __byte_perm(v2, v3, hf ? 0x7632 : 0x5410);
+            const uint32_t x8 = x >> 8, y8 = y >> 8;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(o[nt][g][2 * hf], a0, a1, a2, a3, bf[nt][0], bf[nt][1]);
-              mma_bf16(o[nt][g][2 * hf + 1], e0, e1, e2, e3, bf[nt][0], bf[nt][1]);
+              float(&oa)[4] = o[nt][g][2 * hf], (&ob)[4] = o[nt][g][2 * hf + 1];
+              mma_bf16(oa, codes_lo(x), codes_hi(x), codes_lo(y), codes_hi(y), bf[nt][0],
+                       bf[nt][1]);
+              mma_bf16(ob, codes_lo(x8), codes_hi(x8), codes_lo(y8), codes_hi(y8), bf[nt][0],
+                       bf[nt][1]);
+              mma_bf16(oa, kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
+              mma_bf16(ob, kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
             }
           }
         }
       }
     }
     // ------------------------------------------------------ merge the warps
+    // log-sum-exp of a head, and what its O is divided by (for store())
+    auto finish = [&](int h, float M, float L) {
+      s_inv[h] = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays
+      if (h >= heads) return;
+      const float l2 = L > 0.f ? M + (log2f(L) - kShift) : (L == 0.f ? -INFINITY : L);
+      if (P.lse) P.lse[(int64_t)(h0 + h) * c.B + seg.b] = l2 * 0.6931471805599453f;
+      if (P.lse2) P.lse2[(int64_t)seg.b * P.Hq + h0 + h] = l2;
+    };
+    auto store = [&](int e, const float4& num) {  // four channels of a head
+      const int h = e / D;
+      if (h >= heads) return;
+      const float inv = s_inv[h];
+      *reinterpret_cast<uint2*>(P.O + (int64_t)seg.b * P.q_stride + (int64_t)h0 * D + e) =
+          make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+    };
     __syncwarp();
     float* part = nullptr;
     if (last_stage >= 0) {
@@ -549,52 +606,47 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
             float rs = r[nt][g][y];
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, s);
-            rs = fmaf(-24.f, lw[nt][g][y], rs);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               *reinterpret_cast<float2*>(part + h * D + 64 * g + 8 * gid + 2 * j) = make_float2(
-                  fmaf(16.f, o[nt][g][j][y], rs), fmaf(16.f, o[nt][g][j][y + 2], rs));
+                  fmaf(o[nt][g][j][y] * 0x1p100f, 0x1p33f, rs),
+                  fmaf(o[nt][g][j][y + 2] * 0x1p100f, 0x1p29f, rs));  // odd codes: 16 n
           }
         }
     }
     if (lane == 0) s_part[warp] = part;
     __syncthreads();
     const bool shared = k0 > 0 || k1 < seg.v.pages;
-    const int row_id = seg.b * RPS + seg.row;
     // a CTA has at most two shared rows: the one its range starts in and the
     // one it ends in
     float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * (HT * (D + 2));
-    auto store = [&](int h, int ch, float M, float L, float num) {
-      if (h >= heads) return;
-      const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays
-      P.O[(int64_t)seg.b * P.q_stride + (int64_t)(h0 + h) * D + ch] = __float2bfloat16_rn(num * inv);
-      if (ch == 0) {
-        const float l2 = L > 0.f ? M + log2f(L) : (L == 0.f ? -INFINITY : L);
-        if (P.lse) P.lse[(int64_t)(h0 + h) * c.B + seg.b] = l2 * 0.6931471805599453f;
-        if (P.lse2) P.lse2[(int64_t)seg.b * P.Hq + h0 + h] = l2;
-      }
-    };
-    for (int e = tid; e < HT * D; e += kDecThreads) {
-      const int h = e / D, ch = e % D;
-      float M = -INFINITY, L = 0.f, num = 0.f;
+    if (tid < HT) {  // the warps' factors for this head
+      float M = -INFINITY, L = 0.f;
       for (int w = 0; w < kDecWarps; ++w)
-        if (s_part[w]) M = fmaxf(M, s_part[w][HT * D + h]);
+        if (s_part[w]) M = fmaxf(M, s_part[w][HT * D + tid]);
       const float Mb = M == -INFINITY ? 0.f : M;
       for (int w = 0; w < kDecWarps; ++w)
         if (s_part[w]) {
-          const float fw = ex2_approx(s_part[w][HT * D + h] - Mb);
-          L = fmaf(fw, s_part[w][HT * D + HT + h], L);
-          num = fmaf(fw, s_part[w][e], num);
+          const float fw = ex2_approx(s_part[w][HT * D + tid] - Mb);
+          s_fac[w][tid] = fw;
+          L = fmaf(fw, s_part[w][HT * D + HT + tid], L);
         }
-      if (!shared) {
-        store(h, ch, M, L, num);
+      if (shared) {
+        out[HT * D + tid] = M;
+        out[HT * D + HT + tid] = L;
       } else {
-        out[e] = num;
-        if (ch == 0) {
-          out[HT * D + h] = M;
-          out[HT * D + HT + h] = L;
-        }
+        finish(tid, M, L);
       }
+    }
+    __syncthreads();
+    for (int e = 4 * tid; e < HT * D; e += 4 * kDecThreads) {
+      const int h = e / D;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kDecWarps; ++w)
+        if (s_part[w])
+          axpy(num, s_fac[w][h], *reinterpret_cast<const float4*>(s_part[w] + e));
+      if (shared) *reinterpret_cast<float4*>(out + e) = num;
+      else store(e, num);
     }
     if (shared) {
       // list positions of the row give the CTAs that share it
@@ -602,7 +654,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       const int c0 = row0 / share, c1 = (row1 - 1) / share;
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(P.ticket + row_id, 1) == c1 - c0;
+      if (tid == 0)
+        s_last = atomicAdd(P.ticket + seg.b * RPS + seg.row, 1) == c1 - c0;
       __syncthreads();
       if (s_last) {
         __threadfence();
@@ -610,18 +663,59 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
         auto part_of = [&](int x) {
           return P.parts + (size_t)(2 * x + ((int64_t)x * share < row0 ? 1 : 0)) * (HT * (D + 2));
         };
-        for (int e = tid; e < HT * D; e += kDecThreads) {
-          const int h = e / D, ch = e % D;
-          float M = -INFINITY, L = 0.f, num = 0.f;
-          for (int x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(part_of(x) + HT * D + h));
-          const float Mb = M == -INFINITY ? 0.f : M;
-          for (int x = c0; x <= c1; ++x) {
-            const float* px = part_of(x);
-            const float fx = ex2_approx(__ldcg(px + HT * D + h) - Mb);
-            L = fmaf(fx, __ldcg(px + HT * D + HT + h), L);
-            num = fmaf(fx, __ldcg(px + e), num);
+        // a warp per head: maximum over the parts, then their factors, in
+        // pieces of kDecWarps parts (s_fac's size), added in the parts' order
+        float4 num[kJoin];
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) num[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tid < HT) s_join[tid] = 0.f;
+        for (int h = warp; h < HT; h += kDecWarps) {
+          float M = -INFINITY;
+          for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HT * D + h));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          if (lane == 0) s_join[HT + h] = M;
+        }
+        for (int x0 = c0; x0 <= c1; x0 += kDecWarps) {
+          const int parts = min(kDecWarps, c1 - x0 + 1);
+          __syncthreads();
+          for (int e = tid; e < kDecWarps * HT; e += kDecThreads) {
+            const int x = e / HT, h = e % HT;
+            if (x < parts) {
+              const float M = s_join[HT + h], Mb = M == -INFINITY ? 0.f : M;
+              const float* px = part_of(x0 + x) + HT * D + h;
+              const float fx = ex2_approx(__ldcg(px) - Mb);
+              s_fac[x][h] = fx;
+              s_sumw[x][h] = fx * __ldcg(px + HT);
+            }
           }
-          store(h, ch, M, L, num);
+          __syncthreads();
+          if (tid < HT)
+            for (int x = 0; x < parts; ++x) s_join[tid] += s_sumw[x][tid];
+#pragma unroll
+          for (int q = 0; q < kJoin; ++q) {
+            const int e = 4 * (tid + q * kDecThreads);
+            if (e < HT * D) {
+              float4 y[kDecWarps];
+#pragma unroll
+              for (int x = 0; x < kDecWarps; ++x)
+                if (x < parts) y[x] = __ldcg(reinterpret_cast<const float4*>(part_of(x0 + x) + e));
+#pragma unroll
+              for (int x = 0; x < kDecWarps; ++x)
+                if (x < parts) axpy(num[q], s_fac[x][e / D], y[x]);
+            }
+          }
+        }
+        __syncthreads();
+        if (tid < HT) {
+          const float M = s_join[HT + tid], L = s_join[tid];
+          finish(tid, M, L);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kJoin; ++q) {
+          const int e = 4 * (tid + q * kDecThreads);
+          if (e < HT * D) store(e, num[q]);
         }
       }
     }
@@ -658,8 +752,8 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const 
       float w = 0.f;
       for (int h = 0; h < P.G; h += 2) {
         const float2 x = *reinterpret_cast<const float2*>(s + h);
-        w += ex2_approx(fmaf(x.x, P.scale, -__ldg(lse2 + h)));
-        if (h + 1 < P.G) w += ex2_approx(fmaf(x.y, P.scale, -__ldg(lse2 + h + 1)));
+        w += ex2_approx(x.x - __ldg(lse2 + h));
+        if (h + 1 < P.G) w += ex2_approx(x.y - __ldg(lse2 + h + 1));
       }
       sum += w;
     }
@@ -697,7 +791,7 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
   P.G = a.G;
   P.HC = L.HC;
   P.Gp = L.Gp;
-  P.scale = a.scale * (16.f * 1.4426950408889634f);
+  P.scale = a.scale * 1.4426950408889634f;
   P.window = a.window;
   P.sinks = a.sinks;
   P.O = static_cast<__nv_bfloat16*>(a.O);

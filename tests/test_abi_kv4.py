@@ -93,6 +93,7 @@ def test_decode_arguments():
     assert _decode(qs=500) == vs.VS_ERR_INVALID_ARG
     assert _decode(qs=516) == vs.VS_ERR_UNSUPPORTED
     assert _decode(Q=_fake(0x10008)) == vs.VS_ERR_UNSUPPORTED
+    assert _decode(O=_fake(0x10008)) == vs.VS_ERR_UNSUPPORTED
     assert _decode(scale=-1.0) == vs.VS_ERR_INVALID_ARG
     assert _decode(scale=float("nan")) == vs.VS_ERR_INVALID_ARG
     assert _decode(window=-1) == vs.VS_ERR_INVALID_ARG

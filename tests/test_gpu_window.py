@@ -1,9 +1,9 @@
 """Sliding-window attention with visible first keys vs the fp64 oracle (the window as the slash
 offsets below it, the first keys as vertical columns), single sequences and packed batches.
 
-Tolerance of O: P is rounded to bf16 before the product with V (half a step, 2^-9 of each weight) and
-O once at the end (2^-9 of the value), so |err| <= 2^-9 max|V| + 2^-9 max|V|; the fp32 sums, the
-exponential and the log-sum-exp are off by less than 1e-4 at these sizes (scores below 32, at most
+Tolerance of O: P is rounded to bf16 before the product with V (half a step, finfo(bfloat16).eps / 2 =
+2^-8 of each weight) and O once at the end (2^-8 of the value), so |err| <= 2^-8 max|V| + 2^-8 max|V|;
+the fp32 sums, the exponential and the log-sum-exp are off by less than 1e-4 at these sizes (scores below 32, at most
 128 fp32 additions per score)."""
 import numpy as np
 import pytest
@@ -22,7 +22,7 @@ def _check(O, lse, Qb, Kb, Vb, window, sinks, what=""):
     N, Hq, _ = Qb.shape
     vi, vc = sets_to_rows([np.arange(min(sinks, N))])
     si, sc = sets_to_rows([np.arange(min(window, N))])
-    tol = 2.0 ** -8 * np.abs(bf16_bits_to_f32(Vb)).max() + 1e-4
+    tol = 2.0 ** -7 * np.abs(bf16_bits_to_f32(Vb)).max() + 1e-4
     for h in sorted({0, Hq // 2, Hq - 1}):
         Or, lr = oracle.attn_rows(Qb, Kb, Vb, h, np.arange(N), vi, vc, si, sc)
         err = np.abs(O[:, h] - Or).max()
