@@ -38,13 +38,26 @@
 
 namespace vs {
 
-constexpr int kDecWarps = 12;
-constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecStages = 2;
+// Compute warps (and one more that issues the copies): four warps a scheduler
+// leave 128 registers a thread, enough for 8 query heads a row; the
+// accumulators of 16 need the 255 of two a scheduler.  The warps of a team take
+// a page together, so that fewer of the ring's slots (what 216 KB of shared
+// memory hold) are in use and more are being filled.
+template <int GR, int NT>
+struct DecodeShape {
+  static constexpr int kWarps = NT == 1 ? 15 : 7;
+  static constexpr int kTeam = 1;
+  static constexpr int kTeams = kWarps / kTeam;
+  static constexpr int kSlots = 48 / GR;
+  static constexpr int kCompute = 32 * kWarps;  // compute threads
+  static constexpr int kThreads = kCompute + 32;
+  static constexpr int kFetch = 4;  // pages issued together
+  static_assert(kSlots > kTeams + kFetch && 32 % kFetch == 0, "see the copying warp");
+};
 // The weights carry 2^kShift: V steps s from 2^-40 (below, the products with
 // codes of 2^-133 lose bits) to 2^60 (above, sums over long rows overflow).
 constexpr float kShift = 48.f;
-constexpr int kDecMinPages = kDecWarps;  // per CTA: below, warps would idle beside idle CTAs
+constexpr int kDecMinPages = 8;  // per CTA, where the list is short
 
 // Workspace: status and tickets (zeroed by the call), then parts, the rows'
 // log2-sum-exp and the scores (the last two only where weights are asked for).
@@ -166,8 +179,8 @@ __device__ __forceinline__ void axpy(float4& y, float a, const float4& x) {
 
 // Where a CTA's or warp's walk over the list of pages stands.
 struct Cursor {
-  int b, row;  // sequence, and (KV head, head chunk) of it
-  int k;       // page in the row's list
+  int b, head, hc;  // sequence, KV head, chunk of its query heads
+  int k;            // page in the row's list
   Visible v;
 };
 
@@ -181,27 +194,36 @@ __device__ __forceinline__ void cursor_add(const DecodeParams& P, Cursor& q, int
   q.k += by;
   while (q.k >= q.v.pages) {
     q.k -= q.v.pages;
-    if (++q.row == P.c.Hkv * P.HC) {
-      q.row = 0;
-      do {
-        if (++q.b >= P.c.B) return;
-        cursor_load(P, q);
-      } while (q.v.pages == 0);
-    }
+    if (++q.hc < P.HC) continue;
+    q.hc = 0;
+    if (++q.head < P.c.Hkv) continue;
+    q.head = 0;
+    do {
+      if (++q.b >= P.c.B) return;
+      cursor_load(P, q);
+    } while (q.v.pages == 0);
   }
 }
 
 template <int GR, int NT>
-__global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const DecodeParams P) {
+__global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
+    kv4_decode_kernel(const DecodeParams P) {
   constexpr int D = 64 * GR, HT = 8 * NT;
+  using Shape = DecodeShape<GR, NT>;
+  constexpr int kDecWarps = Shape::kWarps, kSlots = Shape::kSlots, kDecThreads = Shape::kCompute;
+  constexpr int kTeam = Shape::kTeam, kTeams = Shape::kTeams, kFetch = Shape::kFetch;
+  // floats of a warp's part of a row: O [HT][D], m and l [HT]
+  constexpr int kPart = HT * (D + 2);
   constexpr int kChunk = GR * kKv4GroupBytes;
+  constexpr int TT = 2;  // tiles a step: their chains of dependent instructions overlap
   extern __shared__ __align__(128) uint8_t smem[];
-  // ring [warp][stage][kChunk]; a warp's last consumed stage of a row also
-  // carries its part (O [HT][D], m and l [HT]) to the merge
-  static_assert(sizeof(float) * HT * (D + 2) <= kChunk, "a part fits a stage");
-  __shared__ __align__(8) uint64_t bars[kDecWarps * kDecStages];
+  // ring [slot][kChunk]; the slot of a team's last page of a row also carries
+  // its warps' parts to the merge
+  static_assert(sizeof(float) * kTeam * kPart <= kChunk, "the parts fit a slot");
+  __shared__ __align__(8) uint64_t bars[2 * kSlots];  // full, empty
+  __shared__ bool s_valid[kSlots];                    // a page of the pool
   __shared__ int s_abort, s_last;
-  __shared__ int s_sum[kDecWarps];
+  __shared__ int s_sum[kDecWarps + 1];
   __shared__ int s_start[2];
   __shared__ const float* s_part[kDecWarps];
   __shared__ float s_fac[kDecWarps][HT], s_sumw[kDecWarps][HT], s_join[2 * HT], s_inv[HT];
@@ -213,12 +235,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
 
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < kDecWarps * kDecStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(smem_u32(&bars[i]), i < kSlots ? 1 : kTeam);
     fence_mbar_init();
   }
   // the list's length, and where this CTA's range starts: thread i sums a
   // contiguous piece of the sequences
-  const int per = (c.B + kDecThreads - 1) / kDecThreads;
+  constexpr int kAll = Shape::kThreads;
+  const int per = (c.B + kAll - 1) / kAll;
   const int b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
   int mine = 0;
   for (int b = b0; b < b1; ++b) {
@@ -237,7 +260,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
   __syncthreads();
   int total = 0, before = incl - mine;
 #pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
+  for (int w = 0; w <= kDecWarps; ++w) {
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
@@ -264,10 +287,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
     int n;
     kv4_len(c, b, n);
     if (n > 0) continue;
-    for (int e = tid; e < P.Hq * D; e += kDecThreads)
+    for (int e = tid; e < P.Hq * D; e += kAll)
       P.O[(int64_t)b * P.q_stride + e] = __float2bfloat16_rn(0.f);
     if (P.lse)
-      for (int h = tid; h < P.Hq; h += kDecThreads) P.lse[(int64_t)h * c.B + b] = -INFINITY;
+      for (int h = tid; h < P.Hq; h += kAll) P.lse[(int64_t)h * c.B + b] = -INFINITY;
   }
   __syncthreads();
   if (f0 >= f1) return;
@@ -275,44 +298,87 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
   Cursor seg;  // the CTA's walk, row by row
   seg.b = s_start[0];
   cursor_load(P, seg);
-  seg.row = s_start[1] / seg.v.pages;
   seg.k = s_start[1] % seg.v.pages;
-  Cursor next = seg;  // the next page this warp fetches
+  seg.head = s_start[1] / seg.v.pages / P.HC;
+  seg.hc = s_start[1] / seg.v.pages % P.HC;
   const int count = f1 - f0;
-  int issued = warp;  // its place in the CTA's range
-  if (issued < count) cursor_add(P, next, warp);
-
   const WaitCtx wc{P.wait_limit_ns, P.status, &s_abort};
-  uint8_t* ring = smem + warp * kDecStages * kChunk;
-  auto bar = [&](int s) { return smem_u32(&bars[warp * kDecStages + s]); };
-  uint32_t nissue = 0, nwait = 0;  // copies issued and awaited so far
-  uint32_t valid = 0;              // bit s: stage s holds a page of the pool
-  auto issue = [&]() {
-    if (issued >= count) return;
-    const int st = nissue % kDecStages;
-    const int page = next.k < next.v.first ? next.k : next.k + next.v.gap;
-    const uint8_t* src = kv4_page(c, next.b, page, next.row / P.HC);
-    valid = src ? valid | (1u << st) : valid & ~(1u << st);
-    if (lane == 0) {
-      if (src) {
-        mbar_arrive_expect_tx(bar(st), kChunk);
-        bulk_load(smem_u32(ring + st * kChunk), src, kChunk, bar(st));
-      } else {
-        atomicOr(P.status, VS_DEVFLAG_BOUNDS);
-        mbar_arrive(bar(st));
-      }
-    }
-    ++nissue;
-    issued += kDecWarps;
-    if (issued < count) cursor_add(P, next, kDecWarps);
-  };
-  for (int s = 0; s < kDecStages; ++s) issue();
+  // Page i of the CTA's range goes to slot i mod kSlots and to team i mod kTeams.
+  auto full = [&](int slot) { return smem_u32(&bars[slot]); };
+  auto empty = [&](int slot) { return smem_u32(&bars[kSlots + slot]); };
 
+  if (warp == kDecWarps) {
+    // ------------------------------------------------------- copies
+    // Lane q looks up the pages q, q + 32, ...; the whole warp waits for the
+    // slots of kFetch pages, one after the other, and their lanes issue.  A
+    // slot that a merge holds back is among its row's last kTeams pages; all
+    // pages of that row are issued by then, for the ring has more slots than
+    // kTeams + kFetch.
+    auto source = [&]() {
+      return kv4_page(c, seg.b, seg.k < seg.v.first ? seg.k : seg.k + seg.v.gap, seg.head);
+    };
+    const uint8_t* src = nullptr;
+    if (lane < count) {
+      cursor_add(P, seg, lane);
+      src = source();
+    }
+    int i = 0, slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int base = 0; base < count && ok; base += 32) {
+      const uint8_t* next = nullptr;  // looked up ahead of the waits
+      if (base + 32 + lane < count) {
+        cursor_add(P, seg, 32);
+        next = source();
+      }
+      for (; i < min(count, base + 32); i += kFetch) {
+        int mine = 0, at = slot;  // this lane's slot
+#pragma unroll
+        for (int q = 0; q < kFetch; ++q) {
+          if (i + q >= kSlots && i + q < count)
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(empty(at), phase ^ 1u, wc));
+          if (lane == i - base + q) mine = at;
+          if (++at == kSlots) {
+            at = 0;
+            phase ^= 1u;
+          }
+        }
+        slot = at;
+        if (!ok) break;
+        if (lane >= i - base && lane < i - base + kFetch && base + lane < count) {
+          s_valid[mine] = src != nullptr;
+          if (src) {
+            mbar_arrive_expect_tx(full(mine), kChunk);
+            bulk_load(smem_u32(smem + mine * kChunk), src, kChunk, full(mine));
+          } else {
+            atomicOr(P.status, VS_DEVFLAG_BOUNDS);
+            mbar_arrive(full(mine));
+          }
+        }
+        __syncwarp();
+      }
+      src = next;
+    }
+    // every copy lands before shared memory is released: the ring's last turn
+    // (the earlier ones have been used up)
+    i = min(i, count);
+    for (int x = max(0, i - kSlots); x < i; ++x)
+      mbar_wait_drain(full(x % kSlots), (uint32_t)(x / kSlots) & 1u, P.wait_limit_ns);
+    return;
+  }
+
+  const int team = warp / kTeam, member = warp % kTeam;
+  int slot = team;  // of the team's next page
+  uint32_t phase = 0;
+  auto compute_sync = [&]() {  // the compute warps, each converged
+    __syncwarp();
+    named_bar_sync(1, kDecThreads);
+  };
   bool ok = true;
   for (int at = 0; at < count;) {
     // ---------------------------------------------- one row, pages [k0, k1)
     const int k0 = seg.k, k1 = min(seg.v.pages, k0 + (count - at));
-    const int head = seg.row / P.HC, hc = seg.row % P.HC;
+    const int head = seg.head, hc = seg.hc;
     int n;
     kv4_len(c, seg.b, n);
     const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
@@ -390,26 +456,27 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = nb[nt][0] = nb[nt][1] = 0.f;
     }
-    int last_stage = -1;
-    // this warp's pages of the row
-    for (int i = at + (warp + kDecWarps - at % kDecWarps) % kDecWarps; i < at + (k1 - k0);
-         i += kDecWarps) {
+    int last = -1;  // slot of the team's last page of the row so far
+    // the team's pages of the row
+    for (int i = at + (team + kTeams - at % kTeams) % kTeams; i < at + (k1 - k0); i += kTeams) {
       const int k = k0 + (i - at);
-      if (ok && last_stage >= 0) {  // into the stage consumed before this page
+      if (last >= 0) {
         __syncwarp();
-        issue();
+        if (lane == 0) mbar_arrive(empty(last));
       }
-      const int st = nwait % kDecStages;
-      if (ok) ok = mbar_wait(bar(st), (nwait / kDecStages) & 1, wc);
+      if (ok) ok = mbar_wait(full(slot), phase, wc);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {  // a copy may still be on its way into the stage
-        last_stage = -1;
+      if (!ok) {  // a copy may still be on its way into the slot
+        last = -1;
         continue;
       }
-      ++nwait;
-      last_stage = st;
-      if (!((valid >> st) & 1)) continue;
-      const uint8_t* pg = ring + st * kChunk;
+      last = slot;
+      if ((slot += kTeams) >= kSlots) {
+        slot -= kSlots;
+        phase ^= 1u;
+      }
+      if (!s_valid[last]) continue;
+      const uint8_t* pg = smem + last * kChunk;
       const int page = k < seg.v.first ? k : k + seg.v.gap;
       const int t0 = page * kKv4Page;
       // every slot of the page visible?
@@ -423,20 +490,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       // a cold instruction cache.
       auto perm = [](int x) { return x ^ ((x >> 2) & 1); };
       const int ra = perm(gid);
-      const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, ra) + 8 * tig;
-      const uint8_t* va = pg + kv4_code_off(GR, 1, 0, perm(2 * tig)) + 4 * gid;
-      const uint8_t* vb = pg + kv4_code_off(GR, 1, 0, perm(2 * tig + 1)) + 4 * gid;
-      const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, ra);
       const int tiles = min(4, (n - t0 + 15) / 16);
 #pragma unroll 1
-      for (int tl = 0; tl < tiles; ++tl, kc += 512, va += 512, vb += 512, pr += 64) {
-        float sc[NT][4];
+      for (int tl = TT * member; tl < tiles; tl += TT * kTeam) {
+        const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, 16 * tl + ra) + 8 * tig;
+        const uint8_t* va = pg + kv4_code_off(GR, 1, 0, 16 * tl + perm(2 * tig)) + 4 * gid;
+        const uint8_t* vb = pg + kv4_code_off(GR, 1, 0, 16 * tl + perm(2 * tig + 1)) + 4 * gid;
+        const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, 16 * tl + ra);
+        float sc[TT][NT][4];
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {
-          const uint2 wa = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes);
-          const uint2 wb = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes + 256);
-          const uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs);
-          const uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 32);
+        for (int g = 0; g < GR; ++g)
+#pragma unroll
+        for (int u = 0; u < TT; ++u) {
+          const uint2 wa = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes + 512 * u);
+          const uint2 wb = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes + 512 * u + 256);
+          const uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * u);
+          const uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * u + 32);
           const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
           const float sa = kv4_step(pa), sb = kv4_step(pb);
           const float ma = kv4_min(pa), mb = kv4_min(pb);
@@ -455,17 +524,19 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const float mm = x < 2 ? ma : mb, ss = x < 2 ? sa : sb, qq = qs[nt][g][x & 1];
-              sc[nt][x] = fmaf(ss, cacc[x], g == 0 ? mm * qq : fmaf(mm, qq, sc[nt][x]));
+              sc[u][nt][x] = fmaf(ss, cacc[x], g == 0 ? mm * qq : fmaf(mm, qq, sc[u][nt][x]));
             }
           }
         }
-        const int ta = t0 + 16 * tl + ra, tb = ta + 8;
+        const int ta = t0 + 16 * tl + ra;  // slot of row gid of the first tile
         if (!whole) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (hidden(ta)) sc[nt][0] = sc[nt][1] = -INFINITY;
-            if (hidden(tb)) sc[nt][2] = sc[nt][3] = -INFINITY;
-          }
+          for (int u = 0; u < TT; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (hidden(ta + 16 * u)) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
+              if (hidden(ta + 16 * u + 8)) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
+            }
         }
         if (P.score) {
 #pragma unroll
@@ -473,10 +544,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
             const int hh = hc * HT + 8 * nt + 2 * tig;
             if (hh < P.Gp) {
               float* dst = P.score + (((int64_t)seg.b * c.Hkv + head) * P.slots + ta) * P.Gp + hh;
-              *reinterpret_cast<float2*>(dst) =
-                  make_float2(sc[nt][0] * sl[nt][0], sc[nt][1] * sl[nt][1]);
-              *reinterpret_cast<float2*>(dst + 8 * P.Gp) =
-                  make_float2(sc[nt][2] * sl[nt][0], sc[nt][3] * sl[nt][1]);
+#pragma unroll
+              for (int y = 0; y < 2 * TT; ++y)
+                *reinterpret_cast<float2*>(dst + 8 * y * P.Gp) =
+                    make_float2(sc[y / 2][nt][2 * (y & 1)] * sl[nt][0],
+                                sc[y / 2][nt][2 * (y & 1) + 1] * sl[nt][1]);
             }
           }
         }
@@ -489,7 +561,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            mx[nt][y] = fmaxf(sc[nt][y], sc[nt][y + 2]) * sl[nt][y];
+            float x = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < TT; ++u) x = fmax3(x, sc[u][nt][y], sc[u][nt][y + 2]);
+            mx[nt][y] = x * sl[nt][y];
             need |= mx[nt][y] > m[nt][y] + 8.f;
           }
         if (__any_sync(0xffffffffu, need)) {
@@ -518,38 +593,42 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
               }
             }
         }
-        float p[NT][4];
+        float p[TT][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < TT; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            p[nt][x] = ex2_approx(fmaf(sc[nt][x], sl[nt][x & 1], nb[nt][x & 1]));
-            l[nt][x & 1] += p[nt][x];
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              p[u][nt][x] = ex2_approx(fmaf(sc[u][nt][x], sl[nt][x & 1], nb[nt][x & 1]));
+              l[nt][x & 1] += p[u][nt][x];
+            }
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
 #pragma unroll
         for (int g = 0; g < GR; ++g) {
-          uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs);
-          uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 32);
+          uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * u);
+          uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * u + 32);
           if (!whole) {  // 0 * NaN of a slot never written
-            if (hidden(ta)) pa = 0;
-            if (hidden(tb)) pb = 0;
+            if (hidden(ta + 16 * u)) pa = 0;
+            if (hidden(ta + 16 * u + 8)) pb = 0;
           }
           const float sa = kv4_step(pa), sb = kv4_step(pb);
           const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
           uint32_t bf[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            bf[nt][0] = transpose8(pack_bf16x2(p[nt][0] * sa, p[nt][1] * sa));
-            bf[nt][1] = transpose8(pack_bf16x2(p[nt][2] * sb, p[nt][3] * sb));
+            bf[nt][0] = transpose8(pack_bf16x2(p[u][nt][0] * sa, p[u][nt][1] * sa));
+            bf[nt][1] = transpose8(pack_bf16x2(p[u][nt][2] * sb, p[u][nt][3] * sb));
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-              r[nt][g][y] = fmaf(p[nt][y], ca, fmaf(p[nt][y + 2], cb, r[nt][g][y]));
+              r[nt][g][y] = fmaf(p[u][nt][y], ca, fmaf(p[u][nt][y + 2], cb, r[nt][g][y]));
           }
           // V^T as the A operand: channel rows of word gid, slots in pairs
-          const uint32_t v0 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes);
-          const uint32_t v1 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes);
-          const uint32_t v2 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes + 256);
-          const uint32_t v3 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes + 256);
+          const uint32_t v0 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes + 512 * u);
+          const uint32_t v1 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes + 512 * u);
+          const uint32_t v2 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes + 512 * u + 256);
+          const uint32_t v3 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes + 512 * u + 256);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint32_t x = __byte_perm(v0, v1, hf ? 0x7632 : 0x5410);
@@ -585,10 +664,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       *reinterpret_cast<uint2*>(P.O + (int64_t)seg.b * P.q_stride + (int64_t)h0 * D + e) =
           make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
     };
-    __syncwarp();
+    compute_sync();  // the other warp of the team may still read the slot
     float* part = nullptr;
-    if (last_stage >= 0) {
-      part = reinterpret_cast<float*>(ring + last_stage * kChunk);
+    if (last >= 0) {
+      part = reinterpret_cast<float*>(smem + last * kChunk) + member * kPart;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -615,11 +694,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
         }
     }
     if (lane == 0) s_part[warp] = part;
-    __syncthreads();
+    compute_sync();
     const bool shared = k0 > 0 || k1 < seg.v.pages;
     // a CTA has at most two shared rows: the one its range starts in and the
     // one it ends in
-    float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * (HT * (D + 2));
+    float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * kPart;
     if (tid < HT) {  // the warps' factors for this head
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < kDecWarps; ++w)
@@ -638,7 +717,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
         finish(tid, M, L);
       }
     }
-    __syncthreads();
+    compute_sync();
     for (int e = 4 * tid; e < HT * D; e += 4 * kDecThreads) {
       const int h = e / D;
       float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -653,15 +732,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
       const int row0 = f0 + at - k0, row1 = row0 + seg.v.pages;
       const int c0 = row0 / share, c1 = (row1 - 1) / share;
       __threadfence();
-      __syncthreads();
+      compute_sync();
       if (tid == 0)
-        s_last = atomicAdd(P.ticket + seg.b * RPS + seg.row, 1) == c1 - c0;
-      __syncthreads();
+        s_last = atomicAdd(P.ticket + (seg.b * c.Hkv + seg.head) * P.HC + seg.hc, 1) == c1 - c0;
+      compute_sync();
       if (s_last) {
         __threadfence();
         // CTA x's part is its first unless its range starts before the row
         auto part_of = [&](int x) {
-          return P.parts + (size_t)(2 * x + ((int64_t)x * share < row0 ? 1 : 0)) * (HT * (D + 2));
+          return P.parts + (size_t)(2 * x + ((int64_t)x * share < row0 ? 1 : 0)) * kPart;
         };
         // a warp per head: maximum over the parts, then their factors, in
         // pieces of kDecWarps parts (s_fac's size), added in the parts' order
@@ -678,7 +757,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
         }
         for (int x0 = c0; x0 <= c1; x0 += kDecWarps) {
           const int parts = min(kDecWarps, c1 - x0 + 1);
-          __syncthreads();
+          compute_sync();
           for (int e = tid; e < kDecWarps * HT; e += kDecThreads) {
             const int x = e / HT, h = e % HT;
             if (x < parts) {
@@ -689,29 +768,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
               s_sumw[x][h] = fx * __ldcg(px + HT);
             }
           }
-          __syncthreads();
+          compute_sync();
           if (tid < HT)
             for (int x = 0; x < parts; ++x) s_join[tid] += s_sumw[x][tid];
 #pragma unroll
           for (int q = 0; q < kJoin; ++q) {
             const int e = 4 * (tid + q * kDecThreads);
             if (e < HT * D) {
-              float4 y[kDecWarps];
-#pragma unroll
-              for (int x = 0; x < kDecWarps; ++x)
-                if (x < parts) y[x] = __ldcg(reinterpret_cast<const float4*>(part_of(x0 + x) + e));
-#pragma unroll
-              for (int x = 0; x < kDecWarps; ++x)
-                if (x < parts) axpy(num[q], s_fac[x][e / D], y[x]);
+#pragma unroll 4
+              for (int x = 0; x < parts; ++x)
+                axpy(num[q], s_fac[x][e / D],
+                     __ldcg(reinterpret_cast<const float4*>(part_of(x0 + x) + e)));
             }
           }
         }
-        __syncthreads();
+        compute_sync();
         if (tid < HT) {
           const float M = s_join[HT + tid], L = s_join[tid];
           finish(tid, M, L);
         }
-        __syncthreads();
+        compute_sync();
 #pragma unroll
         for (int q = 0; q < kJoin; ++q) {
           const int e = 4 * (tid + q * kDecThreads);
@@ -719,19 +795,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) kv4_decode_kernel(const Decode
         }
       }
     }
-    __syncthreads();  // the parts in the ring are read
-    if (last_stage >= 0) {
+    compute_sync();  // the parts in the ring are read
+    if (last >= 0) {
       fence_proxy_async_smem();  // generic accesses of the stage before its next copy
       __syncwarp();
-      issue();
+      if (lane == 0) mbar_arrive(empty(last));
     }
     at += k1 - k0;
     if (at < count) cursor_add(P, seg, k1 - k0);
   }
-  // copies not awaited (only after a wait gave up) land before shared memory is released
-  if (lane == 0)
-    for (; nwait < nissue; ++nwait)
-      mbar_wait_drain(bar(nwait % kDecStages), (nwait / kDecStages) & 1, P.wait_limit_ns);
 }
 
 // acc_out = acc_in + sum over the KV head's query heads of the softmax weight,
@@ -768,10 +840,11 @@ size_t kv4_decode_ws_bytes(int B, int Hq, int Hkv, int d, int max_len, bool weig
 template <int GR, int NT>
 static cudaError_t launch_decode_impl(const DecodeParams& P, int grid, cudaStream_t stream) {
   auto kern = kv4_decode_kernel<GR, NT>;
-  constexpr int smem = kDecWarps * kDecStages * GR * kKv4GroupBytes;
+  constexpr int smem =
+      DecodeShape<GR, NT>::kSlots * GR * kKv4GroupBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kDecThreads, smem, stream>>>(P);
+  kern<<<grid, DecodeShape<GR, NT>::kThreads, smem, stream>>>(P);
   return cudaGetLastError();
 }
 
