@@ -9,12 +9,14 @@
 // destinations are disjoint, so all moves run at once, and a cache at its
 // budget moves only as many slots as it lost.
 //
-// Bound by latency and by the weights and positions read once (8 bytes a
-// slot); a cluster of 1 to 8 CTAs takes a row.  Each CTA keeps its slice of
-// the row as order-preserving 32-bit keys in shared memory; the boundary key
-// is found by a most-significant-digit search (digits of 11, 11 and 10 bits)
-// over histograms that the cluster sums through distributed shared memory;
-// then slots are counted and listed by warp ballots in slot order.
+// Two kernels.  The first finds who stays, one cluster of 1 to 8 CTAs a row: each
+// thread keeps up to 32 slots of the row as order-preserving 32-bit keys in
+// registers, the boundary key is found digit by digit (four of 8 bits) over
+// histograms that the cluster sums through distributed shared memory, and
+// ballots in slot order give the lists of holes and of the slots that fill
+// them.  Bound by latency (some ten cluster barriers and the row read once, 8
+// bytes a slot).  The second moves, a few moves in flight per 16 lanes over
+// the whole device: bound by the moved bytes, read and written once.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -23,12 +25,7 @@ namespace vs {
 
 namespace cg = cooperative_groups;
 
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
-constexpr int kEvBins = 2048;
-// a row gets a cluster wide enough for slices of this many slots, up to 8 CTAs
-constexpr int kEvSlice = 4096;
 
 // Larger keys stay first: fixed slots, then +inf .. -inf, then NaN.
 __device__ __forceinline__ uint32_t evict_key(float w, bool fixed) {
@@ -39,21 +36,27 @@ __device__ __forceinline__ uint32_t evict_key(float w, bool fixed) {
 }
 
 struct EvictShared {
-  uint32_t hist[kEvBins];
-  uint32_t warp_a[kEvWarps], warp_b[kEvWarps];
+  uint32_t hist[4][256];  // one per digit, read by the cluster
+  uint32_t merged[256];
+  uint32_t warp_a[32], warp_b[32];
   uint32_t total_a, total_b;  // read by the cluster
-  uint32_t digit, above;
 };
 
-__global__ void __launch_bounds__(kEvThreads) kv4_evict_kernel(Kv4EvictArgs a, int32_t* lists,
-                                                              int64_t list_ld) {
+// kEvThreads threads of V slots each.
+template <int kEvThreads, int V>
+__global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
+    kv4_evict_kernel(Kv4EvictArgs a, int32_t* counts, int32_t* lists, int64_t list_ld) {
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  auto sync_all = [&]() {
+    if (C == 1) __syncthreads();
+    else cl.sync();
+  };
   const Kv4Cache& c = a.c;
+  constexpr int kEvWarps = kEvThreads / 32;
   const int row = blockIdx.x / C;  // b * Hkv + head
   const int b = row / c.Hkv, head = row % c.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  extern __shared__ uint32_t keys[];
   __shared__ EvictShared sh;
   int* status = static_cast<int*>(a.ws);
 
@@ -63,6 +66,7 @@ __global__ void __launch_bounds__(kEvThreads) kv4_evict_kernel(Kv4EvictArgs a, i
     if (rank == 0 && tid == 0) {
       atomicOr(status, VS_DEVFLAG_BOUNDS);
       if (head == 0) a.lens_out[b] = 0;
+      counts[row] = 0;
     }
     return;
   }
@@ -73,190 +77,286 @@ __global__ void __launch_bounds__(kEvThreads) kv4_evict_kernel(Kv4EvictArgs a, i
   int32_t* pos_out = a.pos_out + (int64_t)row * a.ld_out;
   if (rank == 0 && tid == 0 && head == 0) a.lens_out[b] = k;
   if (n == k) {
+    if (rank == 0 && tid == 0) counts[row] = 0;
     for (int t = rank * kEvThreads + tid; t < n; t += C * kEvThreads) {
       acc_out[t] = acc[t];
       pos_out[t] = pos[t];
     }
     return;
   }
-  // this CTA's slots [s0, s1), this warp's [w0, w1), in multiples of 32
+  // this CTA's slots [s0, s1); this warp's [w0, w1), at most 32 V of them;
+  // key j of a lane is slot w0 + 32 j + lane
   const int slice = ((n + C - 1) / C + 31) / 32 * 32;
   const int s0 = min(rank * slice, n), s1 = min(s0 + slice, n);
   const int wper = ((s1 - s0 + kEvWarps - 1) / kEvWarps + 31) / 32 * 32;
   const int w0 = min(s0 + warp * wper, s1), w1 = min(w0 + wper, s1);
   const int64_t newest = (int64_t)a.n_tokens[b] - a.recent;
-  for (int t = s0 + tid; t < s1; t += kEvThreads) {
-    const int p = pos[t];
-    keys[t - s0] = evict_key(acc[t], p < a.sinks || p >= newest);
+  for (int i = tid; i < 4 * 256; i += kEvThreads) sh.hist[i >> 8][i & 255] = 0;
+  uint32_t key[V];
+  {
+    const float* pa = acc + w0 + lane;
+    const int32_t* pp = pos + w0 + lane;
+    float w[V];
+    int p[V];
+    if (w0 + 32 * V <= n) {  // no guards: one address, all loads in flight
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = __ldg(pa + 32 * j);
+#pragma unroll
+      for (int j = 0; j < V; ++j) p[j] = __ldg(pp + 32 * j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool in = w0 + 32 * j + lane < n;
+        w[j] = in ? __ldg(pa + 32 * j) : 0.f;
+        p[j] = in ? __ldg(pp + 32 * j) : 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = evict_key(w[j], p[j] < a.sinks || p[j] >= newest);
   }
-  __syncthreads();
+  auto live = [&](int j) { return w0 + 32 * j + lane < w1; };
 
-  // boundary key: the k-th largest.  `need` slots are still to be found among
-  // those whose key begins with `prefix`.
-  uint32_t prefix = 0, need = k;
-  int shift = 32;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10, bins = 1 << bits;
-    const int high = shift;  // bits above this digit are fixed to prefix
-    shift -= bits;
-    for (int i = tid; i < bins; i += kEvThreads) sh.hist[i] = 0;
-    __syncthreads();
-    for (int t = tid; t < s1 - s0; t += kEvThreads) {
-      const uint32_t x = keys[t];
-      if (pass == 0 || (x >> high) == prefix) atomicAdd(&sh.hist[(x >> shift) & (bins - 1)], 1u);
-    }
-    cl.sync();
-    // sums over the cluster, thread i taking bins of its own contiguous piece,
-    // highest bins first
-    const int per = bins / kEvThreads;  // 4 or 2
-    uint32_t mine = 0, part[4];
-    for (int j = 0; j < per; ++j) {
-      const int bin = bins - 1 - (tid * per + j);
+  // Boundary key: the k-th largest.  `need` slots are still to be found among
+  // the `equal` ones whose key begins with `prefix`.
+  uint32_t prefix = 0, need = k, equal = n;
+  __syncthreads();  // the histograms are zero
+#pragma unroll
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (live(j) && (pass == 0 || (key[j] >> (shift + 8)) == prefix))
+        atomicAdd(&sh.hist[pass][(key[j] >> shift) & 255u], 1u);
+    sync_all();
+    if (tid < 256) {
       uint32_t x = 0;
-      for (int r = 0; r < C; ++r) x += cl.map_shared_rank(sh.hist, r)[bin];
-      part[j] = x;
-      mine += x;
+      for (int r = 0; r < C; ++r) x += cl.map_shared_rank(sh.hist[pass], r)[tid];
+      sh.merged[32 * ((255 - tid) & 7) + ((255 - tid) >> 3)] = x;  // as it is read below
     }
-    // exclusive prefix over the threads
+    __syncthreads();
+    // every warp takes the same decision: lane l holds bins 255 - 8 l downwards
+    uint32_t part[8], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      part[i] = sh.merged[32 * i + lane];  // bin 255 - (8 lane + i)
+      mine += part[i];
+    }
     uint32_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) sh.warp_a[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += sh.warp_a[w];
-    for (int j = 0; j < per; ++j) {
-      if (before < need && need <= before + part[j]) {
-        sh.digit = bins - 1 - (tid * per + j);
-        sh.above = before;
+    uint32_t before = incl - mine, digit = 0, count = 0, above = 0;
+    const bool here = before < need && need <= incl;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (before < need && need <= before + part[i]) {
+        digit = 255 - (8 * lane + i);
+        count = part[i];
+        above = before;
       }
-      before += part[j];
+      before += part[i];
     }
-    cl.sync();  // also: the histograms are read before they are cleared
-    prefix = (prefix << bits) | sh.digit;
-    need -= sh.above;
+    const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;  // need <= the sum of all bins
+    prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, from);
+    equal = __shfl_sync(0xffffffffu, count, from);
+    need -= __shfl_sync(0xffffffffu, above, from);
   }
-  const uint32_t bound = prefix;  // `need` of the slots with this key stay, the lowest ones
+  const uint32_t bound = prefix;  // `need` of the `equal` slots with this key stay, the lowest
 
-  // ranks in slot order: of boundary keys first, then of holes and movers
+  // this warp's counts x, y -> the counts of all earlier warps of the cluster
   auto exchange = [&](uint32_t x, uint32_t y, uint32_t& before_x, uint32_t& before_y) {
-    // x, y: this warp's counts -> counts of all earlier warps of the cluster
     if (lane == 0) {
       sh.warp_a[warp] = x;
       sh.warp_b[warp] = y;
     }
     __syncthreads();
-    before_x = before_y = 0;
-    uint32_t all_x = 0, all_y = 0;
-    for (int w = 0; w < kEvWarps; ++w) {
-      if (w == warp) {
-        before_x = all_x;
-        before_y = all_y;
+    uint32_t ax = lane < kEvWarps ? sh.warp_a[lane] : 0u, bx = lane < kEvWarps ? sh.warp_b[lane] : 0u;
+#pragma unroll
+    for (int o = 1; o < kEvWarps; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, ax, o), v = __shfl_up_sync(0xffffffffu, bx, o);
+      if (lane >= o) {
+        ax += u;
+        bx += v;
       }
-      all_x += sh.warp_a[w];
-      all_y += sh.warp_b[w];
     }
-    if (tid == 0) {
-      sh.total_a = all_x;
-      sh.total_b = all_y;
+    before_x = __shfl_sync(0xffffffffu, ax, warp) - x;
+    before_y = __shfl_sync(0xffffffffu, bx, warp) - y;
+    if (C == 1) {
+      __syncthreads();  // read before the next exchange writes
+      return;
+    }
+    if (tid == kEvWarps - 1) {
+      sh.total_a = ax;
+      sh.total_b = bx;
     }
     cl.sync();
-    for (int r = 0; r < rank; ++r) {
-      before_x += *cl.map_shared_rank(&sh.total_a, r);
-      before_y += *cl.map_shared_rank(&sh.total_b, r);
-    }
-    cl.sync();  // read before the next exchange writes
+    uint32_t ox = lane < rank ? *cl.map_shared_rank(&sh.total_a, lane) : 0u;
+    uint32_t oy = lane < rank ? *cl.map_shared_rank(&sh.total_b, lane) : 0u;
+    before_x += __reduce_add_sync(0xffffffffu, ox);
+    before_y += __reduce_add_sync(0xffffffffu, oy);
+    cl.sync();  // read before the next exchange writes, and before any CTA leaves
   };
   const uint32_t below_lane = (1u << lane) - 1u;
-  uint32_t eq = 0, eq_before, none;
-  for (int t = w0 + lane; t - lane < w1; t += 32)
-    eq += __popc(__ballot_sync(0xffffffffu, t < w1 && keys[t - s0] == bound));
-  exchange(eq, 0, eq_before, none);
-  // stays(t) for a warp's 32 slots at once; `seen`: boundary keys before them
-  auto stays = [&](int t, uint32_t& seen) {
-    const uint32_t x = t < w1 ? keys[t - s0] : 0u;
-    const bool tie = t < w1 && x == bound;
-    const uint32_t ties = __ballot_sync(0xffffffffu, tie);
-    const bool s = t < w1 && (x > bound || (tie && seen + __popc(ties & below_lane) < need));
-    seen += __popc(ties);
-    return s;
-  };
-  uint32_t seen = eq_before, holes = 0, movers = 0, hole_at, mover_at;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const bool s = stays(t, seen);
+  uint32_t ties_before = 0;  // boundary keys of earlier warps
+  if (equal != need) {       // uniform over the cluster
+    uint32_t eq = 0, none;
+#pragma unroll
+    for (int j = 0; j < V; ++j) eq += __popc(__ballot_sync(0xffffffffu, live(j) && key[j] == bound));
+    exchange(eq, 0, ties_before, none);
+  }
+  // who stays: bit j of `stay` for key j
+  uint32_t stay = 0;
+  uint32_t holes = 0, movers = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int t = w0 + 32 * j + lane;
+    const bool tie = t < w1 && key[j] == bound;
+    bool s = t < w1 && (key[j] > bound || tie);
+    if (equal != need) {
+      const uint32_t ties = __ballot_sync(0xffffffffu, tie);
+      if (tie && ties_before + __popc(ties & below_lane) >= need) s = false;
+      ties_before += __popc(ties);
+    }
+    if (s) stay |= 1u << j;
     holes += __popc(__ballot_sync(0xffffffffu, t < w1 && t < k && !s));
     movers += __popc(__ballot_sync(0xffffffffu, t >= k && s));
   }
+  uint32_t hole_at, mover_at;
   exchange(holes, movers, hole_at, mover_at);
+  if (rank == C - 1 && warp == kEvWarps - 1 && lane == 0) counts[row] = (int)(hole_at + holes);
   int32_t* hole_list = lists + (int64_t)row * 2 * list_ld;
   int32_t* mover_list = hole_list + list_ld;
-  seen = eq_before;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const bool s = stays(t, seen);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int t = w0 + 32 * j + lane;
+    const bool s = (stay >> j) & 1u;
     const bool hole = t < w1 && t < k && !s, mover = t >= k && s;
     const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
     if (hole) hole_list[hole_at + __popc(hb & below_lane)] = t;
     if (mover) mover_list[mover_at + __popc(mb & below_lane)] = t;
-    if (s && t < k) {
-      acc_out[t] = acc[t];
-      pos_out[t] = pos[t];
-    }
     hole_at += __popc(hb);
     mover_at += __popc(mb);
   }
-  // the moves: as many movers as holes in the whole row
-  if (warp == kEvWarps - 1 && lane == 0) sh.total_b = hole_at;  // this CTA's last warp: all so far
-  __threadfence();
-  cl.sync();
-  const int moves = (int)*cl.map_shared_rank(&sh.total_b, C - 1);
-  // sixteen lanes a move: 16-byte pieces of the codes, then the pairs
-  const int sub = tid & 15, codes = 4 * c.GR;
-  for (int i = (rank * kEvThreads + tid) / 16; i < moves; i += C * kEvThreads / 16) {
-    const int dst = __ldcg(hole_list + i), src = __ldcg(mover_list + i);
-    uint8_t* pd = kv4_page(c, b, dst >> 6, head);
-    const uint8_t* ps = kv4_page(c, b, src >> 6, head);
-    if (!pd || !ps) {
-      if (sub == 0) atomicOr(status, VS_DEVFLAG_BOUNDS);
-    } else if (sub < codes) {  // piece: (K or V, group, half of 32 bytes)
-      const int kv = sub / (2 * c.GR), g = (sub >> 1) % c.GR, off = 16 * (sub & 1);
-      *reinterpret_cast<uint4*>(pd + kv4_code_off(c.GR, kv, g, dst & 63) + off) =
-          *reinterpret_cast<const uint4*>(ps + kv4_code_off(c.GR, kv, g, src & 63) + off);
-    } else if (sub < codes + 2 * c.GR) {
-      const int kv = (sub - codes) / c.GR, g = (sub - codes) % c.GR;
-      *reinterpret_cast<uint32_t*>(pd + kv4_pair_off(c.GR, kv, g, dst & 63)) =
-          *reinterpret_cast<const uint32_t*>(ps + kv4_pair_off(c.GR, kv, g, src & 63));
+  // the entries of the slots that keep their place, a few loads in flight
+  constexpr int kBatch = V < 8 ? V : 8;
+#pragma unroll
+  for (int j0 = 0; j0 < V; j0 += kBatch) {
+    if (w0 + 32 * j0 >= min(k, w1)) break;  // uniform over the warp
+    float w[kBatch];
+    int p[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = 32 * (j0 + j);
+      const bool in = w0 + t + lane < k;  // k <= n
+      w[j] = in ? __ldg(acc + w0 + lane + t) : 0.f;
+      p[j] = in ? __ldg(pos + w0 + lane + t) : 0;
     }
-    if (sub == 14) acc_out[dst] = acc[src];
-    if (sub == 15) pos_out[dst] = pos[src];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = w0 + 32 * (j0 + j) + lane;
+      if (((stay >> (j0 + j)) & 1u) && t < k) {
+        acc_out[t] = w[j];
+        pos_out[t] = p[j];
+      }
+    }
   }
-  cl.sync();  // no CTA leaves while another may still read its shared memory
+}
+
+// The moves of row blockIdx.y: sixteen lanes a move (16-byte pieces of the
+// codes, the pairs, the entries of acc and pos), kMoves moves in flight.
+constexpr int kMoveThreads = 256;
+constexpr int kMoves = 4;
+
+__global__ void __launch_bounds__(kMoveThreads)
+    kv4_move_kernel(Kv4EvictArgs a, const int32_t* counts, const int32_t* lists, int64_t list_ld) {
+  const Kv4Cache& c = a.c;
+  const int row = blockIdx.y, b = row / c.Hkv, head = row % c.Hkv;
+  const int moves = counts[row];
+  const int32_t* hole_list = lists + (int64_t)row * 2 * list_ld;
+  const int32_t* mover_list = hole_list + list_ld;
+  const int groups = gridDim.x * (kMoveThreads / 16);
+  const int sub = threadIdx.x & 15, codes = 4 * c.GR;
+  // what this lane copies: offset of its piece in slot 0's, and per slot
+  int off = 0, step = 0;
+  if (sub < codes) {
+    off = kv4_code_off(c.GR, sub / (2 * c.GR), (sub >> 1) % c.GR, 0) + 16 * (sub & 1);
+    step = 32;
+  } else if (sub < codes + 2 * c.GR) {
+    off = kv4_pair_off(c.GR, (sub - codes) / c.GR, (sub - codes) % c.GR, 0);
+    step = 4;
+  }
+  for (int i0 = blockIdx.x * (kMoveThreads / 16) + threadIdx.x / 16; i0 < moves;
+       i0 += groups * kMoves) {
+    int dst[kMoves], src[kMoves];
+    uint8_t* pd[kMoves];
+    const uint8_t* ps[kMoves];
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      const int i = i0 + u * groups;
+      dst[u] = i < moves ? hole_list[i] : -1;
+      src[u] = i < moves ? mover_list[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      pd[u] = dst[u] >= 0 ? kv4_page(c, b, dst[u] >> 6, head) : nullptr;
+      ps[u] = dst[u] >= 0 ? kv4_page(c, b, src[u] >> 6, head) : nullptr;
+    }
+    uint4 x[kMoves];
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (dst[u] < 0) continue;
+      const int64_t at = (int64_t)row * a.ld_in + src[u];
+      if (sub == 14) {
+        x[u].x = __float_as_uint(__ldg(a.acc_in + at));
+      } else if (sub == 15) {
+        x[u].x = (uint32_t)__ldg(a.pos_in + at);
+      } else if (pd[u] && ps[u]) {
+        const uint8_t* p = ps[u] + off + step * (src[u] & 63);
+        if (step == 32) x[u] = *reinterpret_cast<const uint4*>(p);
+        else if (step == 4) x[u].x = *reinterpret_cast<const uint32_t*>(p);
+      } else if (sub == 0) {
+        atomicOr(static_cast<int*>(a.ws), VS_DEVFLAG_BOUNDS);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMoves; ++u) {
+      if (dst[u] < 0) continue;
+      const int64_t at = (int64_t)row * a.ld_out + dst[u];
+      if (sub == 14) {
+        a.acc_out[at] = __uint_as_float(x[u].x);
+      } else if (sub == 15) {
+        a.pos_out[at] = (int)x[u].x;
+      } else if (pd[u] && ps[u]) {
+        uint8_t* p = pd[u] + off + step * (dst[u] & 63);
+        if (step == 32) *reinterpret_cast<uint4*>(p) = x[u];
+        else if (step == 4) *reinterpret_cast<uint32_t*>(p) = x[u].x;
+      }
+    }
+  }
+}
+
+// As many moves at most: holes are among the `keep` first slots, what fills
+// them among the others.
+static int64_t evict_moves(int max_len, int keep) {
+  if (keep >= max_len) return 0;
+  return keep < max_len - keep ? keep : max_len - keep;
 }
 
 size_t kv4_evict_ws_bytes(int B, int Hkv, int max_len, int keep) {
-  const int64_t list = max_len < keep ? max_len : keep;  // as many holes as slots kept at most
-  return align_up(kStatusBytes + sizeof(int32_t) * 2 * (size_t)B * Hkv * (size_t)list, 256);
+  const size_t rows = (size_t)B * Hkv;
+  return align_up(kStatusBytes + sizeof(int32_t) * rows * (1 + 2 * (size_t)evict_moves(max_len, keep)),
+                  256);
 }
 
-cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
-  cudaError_t e = cudaMemsetAsync(a.ws, 0, sizeof(int), a.stream);
-  if (e != cudaSuccess) return e;
-  int C = 1;
-  while (C < kEvMaxCluster && (int64_t)C * kEvSlice < a.c.max_len) C *= 2;
-  const int64_t slice = (ceil_div(a.c.max_len, C) + 31) / 32 * 32;
-  const size_t smem = sizeof(uint32_t) * (size_t)slice;
-  e = cudaFuncSetAttribute(kv4_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem);
-  if (e != cudaSuccess) return e;
-  const int64_t list = a.c.max_len < a.keep ? a.c.max_len : a.keep;
-  int32_t* lists = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + kStatusBytes);
+template <int kEvThreads, int V>
+static cudaError_t launch_evict_impl(const Kv4EvictArgs& a, int C, int32_t* counts, int32_t* lists,
+                                     int64_t list_ld) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.c.B * a.c.Hkv * C));
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -264,7 +364,35 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_evict_kernel, a, lists, list);
+  return cudaLaunchKernelEx(&cfg, kv4_evict_kernel<kEvThreads, V>, a, counts, lists, list_ld);
+}
+
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
+  cudaError_t e = cudaMemsetAsync(a.ws, 0, sizeof(int), a.stream);
+  if (e != cudaSuccess) return e;
+  const int rows = a.c.B * a.c.Hkv, sms = device_sm_count();
+  int32_t* counts = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + kStatusBytes);
+  int32_t* lists = counts + rows;
+  const int64_t list = evict_moves(a.c.max_len, a.keep);
+  // Rows of up to 8192 slots take one CTA of 512 threads (two fit an SM, and no
+  // cluster barrier is needed).  Longer rows take clusters of 1024 threads:
+  // as many CTAs as the slots need at 16 a thread, more while the device has
+  // SMs to spare; from 131072 slots on, 32 a thread.
+  const int n = a.c.max_len;
+  int C = 1;
+  if (n > 8192)
+    while (C < kEvMaxCluster && (C * 16384 < n || 2 * rows * C <= sms)) C *= 2;
+  if (n <= 2048) e = launch_evict_impl<512, 4>(a, C, counts, lists, list);
+  else if (n <= 8192) e = launch_evict_impl<512, 16>(a, C, counts, lists, list);
+  else if (C * 4096 >= n) e = launch_evict_impl<1024, 4>(a, C, counts, lists, list);
+  else if (C * 16384 >= n) e = launch_evict_impl<1024, 16>(a, C, counts, lists, list);
+  else e = launch_evict_impl<1024, 32>(a, C, counts, lists, list);
+  if (e != cudaSuccess || list == 0) return e;
+  const int64_t per_block = (kMoveThreads / 16) * kMoves;
+  const int64_t want = (list + per_block - 1) / per_block, cap = ceil_div(16LL * sms, rows);
+  kv4_move_kernel<<<dim3((unsigned)(want < cap ? want : cap), rows), kMoveThreads, 0, a.stream>>>(
+      a, counts, lists, list);
+  return cudaGetLastError();
 }
 
 }  // namespace vs
