@@ -513,6 +513,7 @@ size_t vs_kv4_page_bytes(int Hkv, int d); /* 0 for an unsupported d */
  * A sequence that does not fit (a malformed offset, more new tokens than
  * lens[b], lens[b] above 64 table_ld or, with acc or pos, above ld) is not
  * written and sets VS_DEVFLAG_BOUNDS.  ws: 256 bytes, 256-byte aligned.
+ * max_new * Hkv * d / 8 < 2^31 (else VS_ERR_UNSUPPORTED).
  */
 vs_status vs_kv4_append(const void* K, const void* V, vs_dtype dtype, int total_tokens,
                         const int32_t* cu_seqlens, int max_new, int64_t kv_stride_tok, void* pool,
@@ -530,6 +531,7 @@ vs_status vs_kv4_append(const void* K, const void* V, vs_dtype dtype, int total_
  * Rows of no sequence are left as they were.  A sequence whose slots do not
  * all lie in [0, lens[b]) is not written and sets VS_DEVFLAG_BOUNDS, as does a
  * malformed offset.  ws: 256 bytes, 256-byte aligned.
+ * max_read * Hkv * d / 8 < 2^31 (else VS_ERR_UNSUPPORTED).
  */
 vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64_t table_ld,
                       const int32_t* lens, const int32_t* start, int B, int max_len, int Hkv, int d,

@@ -173,12 +173,11 @@ def _check(code: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # an int: the declared argtypes make it a pointer
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -464,34 +463,38 @@ def vs_kv4_evict_workspace_size(B: int, Hkv: int, max_len: int, keep: int) -> in
     return int(lib().vs_kv4_evict_workspace_size(B, Hkv, max_len, keep))
 
 
+_KV4_HEAD_DIM = {4608: 64, 9216: 128}  # bytes per page and head -> d
+
+
 def _kv4_dims(pool):
     """(n_pages, Hkv, d) of a pool [n_pages, Hkv, bytes]."""
-    assert pool.dtype == torch.uint8 and pool.dim() == 3 and pool.is_contiguous()
     n_pages, Hkv, nbytes = pool.shape
-    for d in (64, 128):
-        if vs_kv4_page_bytes(1, d) == nbytes:
-            return n_pages, Hkv, d
-    raise ValueError(f"{nbytes} bytes per page and head are no cache format")
+    assert pool.dtype == torch.uint8 and pool.is_contiguous()
+    d = _KV4_HEAD_DIM.get(nbytes)
+    if d is None:
+        raise ValueError(f"{nbytes} bytes per page and head are no cache format")
+    return n_pages, Hkv, d
 
 
 def _kv4_max(table, max_len=None):
     """The bound on lengths that a page table [B, pages] gives, checked against the caller's."""
-    assert table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1
+    assert table.dtype == torch.int32 and table.stride(1) == 1
     room = min(64 * table.shape[1], 1 << 24)
     if max_len is None:
         return room
     if max_len > room:
         raise ValueError(f"max_len {max_len} is more than the page table holds ({room})")
-    return int(max_len)
+    return max_len
 
 
 def _kv4_rows(t):
     """Row length of an acc or pos tensor [B, Hkv, ld] (its rows may be a slice of longer ones)."""
-    if t is None:
-        return 0
-    assert t.dim() == 3 and (t.shape[2] <= 1 or t.stride(2) == 1)
-    assert t.shape[0] <= 1 or t.stride(0) == t.shape[1] * t.stride(1)
-    return t.stride(1) if t.shape[0] * t.shape[1] > 1 else t.shape[2]
+    B, Hkv, ld = t.shape
+    if t.is_contiguous():
+        return ld
+    sb, sh, s1 = t.stride()
+    assert (ld <= 1 or s1 == 1) and (B <= 1 or sb == Hkv * sh)
+    return sh if B * Hkv > 1 else ld
 
 
 def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=None, A_v=None,
@@ -502,7 +505,8 @@ def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=Non
     n_pages, Hkv, d = _kv4_dims(pool)
     assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and V.stride(0) == K.stride(0)
     B = cu_seqlens.numel() - 1
-    ld = _kv4_rows(acc if acc is not None else pos)
+    rows = acc if acc is not None else pos
+    ld = 0 if rows is None else _kv4_rows(rows)
     assert acc is None or pos is None or _kv4_rows(pos) == ld
     Hq = A_v.shape[0] if A_v is not None else Hkv
     assert A_v is None or (A_v.shape[1] == T and A_v.is_contiguous())
@@ -531,7 +535,7 @@ def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, 
     B, Hq, d = Q.shape
     n_pages, Hkv, dp = _kv4_dims(pool)
     assert dp == d and O.shape == Q.shape and O.stride(0) == Q.stride(0)
-    ld = _kv4_rows(acc_out)
+    ld = 0 if acc_out is None else _kv4_rows(acc_out)
     assert acc_in is None or acc_out is None or _kv4_rows(acc_in) == ld
     _check(lib().vs_kv4_decode_attn_fwd(
         _ptr(Q), _dtype(Q), Q.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),

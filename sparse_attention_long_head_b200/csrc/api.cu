@@ -617,6 +617,8 @@ vs_status vs_kv4_append(const void* K, const void* V, vs_dtype dtype, int total_
   if ((A_v && !acc) || ((acc || pos) && ld < 1)) return VS_ERR_INVALID_ARG;
   if (dtype != VS_BF16 || kv_stride_tok % 8 != 0 || !aligned(K, 16) || !aligned(V, 16))
     return VS_ERR_UNSUPPORTED;
+  // 16-byte pieces of a sequence are counted in 32 bits
+  if ((int64_t)max_new * Hkv * (d / 8) >= ((int64_t)1 << 31)) return VS_ERR_UNSUPPORTED;
   if (ws_bytes < kStatusBytes) return VS_ERR_WORKSPACE;
   a.K = K;
   a.V = V;
@@ -648,6 +650,7 @@ vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64
   if (total_tokens < 1 || max_read < 1 || kv_stride_tok < (int64_t)Hkv * d)
     return VS_ERR_INVALID_ARG;
   if (kv_stride_tok % 8 != 0 || !aligned(K, 16) || !aligned(V, 16)) return VS_ERR_UNSUPPORTED;
+  if ((int64_t)max_read * Hkv * (d / 8) >= ((int64_t)1 << 31)) return VS_ERR_UNSUPPORTED;
   if (ws_bytes < kStatusBytes) return VS_ERR_WORKSPACE;
   a.start = start;
   a.cu = cu_seqlens;

@@ -5,11 +5,12 @@
 //     m = min x,  s = bf16((max x - min x) / 15),
 //     n = clamp(rint((x - m) / s), 0, 15)  (ties to even),  x ~ s n + m.
 // m is exact in bf16 (it is one of the values).  s is rounded to bf16: 15 s
-// then misses the range by at most 15 s 2^-9 = 0.03 s, less than the half
-// step that n itself may be off.  The quotient is formed in fp32 and, where it
-// comes within 1e-4 of a half, again in fp64, so that n is the code of the
-// exact quotient.  s = 0 (a constant group) gives n = 0; an infinity or NaN in
-// the group gives s = m = NaN, so that the group reads back as NaN.
+// then misses the range by at most 15 s 2^-8 = 0.06 s, far less than the half
+// step that n itself may be off.  Both quotients are formed in fp32 and, where
+// that comes next to a border between two results, again in fp64, so that s
+// and n are those of the exact quotients.  s = 0 (a constant group) gives
+// n = 0; an infinity or NaN in the group gives s = m = NaN, so that the group
+// reads back as NaN.
 //
 // Both kernels are bound by memory: 4 d bytes of bf16 K and V and 9/8 d bytes
 // of cache per token and head.  Eight lanes take one group of one slot (16
@@ -61,7 +62,13 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
     return 0u;
   }
   const double lo64 = lo;
-  const __nv_bfloat16 sb = __float2bfloat16_rn((float)(((double)hi - lo64) / 15.0));
+  // (hi - lo) / 15 to within 2^-22: the bf16 it rounds to, unless its low half
+  // is next to 0x8000, it is subnormal or hi - lo overflowed
+  float range = (hi - lo) * (1.f / 15.f);
+  const int low = (int)(__float_as_uint(range) & 0xffffu) - 0x8000;
+  if ((low < 8 && low > -8) || !(range > 1e-30f && range < 1e37f))
+    range = (float)(((double)hi - lo64) / 15.0);
+  const __nv_bfloat16 sb = __float2bfloat16_rn(range);
   const float s = __bfloat162float(sb);
   pair = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
   if (s == 0.f) return 0u;
@@ -80,7 +87,7 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
 
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4AppendArgs a) {
   const Kv4Cache& c = a.c;
-  const int b = blockIdx.y, d = c.GR * 64;
+  const int b = blockIdx.y;
   int64_t tok0;
   int n, len;
   bool ok = seq_range(a.cu, a.total, a.max_new, b, tok0, n);
@@ -92,22 +99,19 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4AppendArgs a
     return;
   }
   const int start = len - n;
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t jobs = (int64_t)n * c.Hkv * c.GR * 8;  // a lane's eight channels of K and of V
-  const uint4* K = static_cast<const uint4*>(a.K);
-  const uint4* V = static_cast<const uint4*>(a.V);
-  for (int64_t base = first - (threadIdx.x & 31); base < jobs; base += stride) {
-    const int64_t e = base + (threadIdx.x & 31);
+  const uint32_t stride = gridDim.x * blockDim.x;
+  const uint32_t first = blockIdx.x * blockDim.x + threadIdx.x;
+  const uint32_t line = c.Hkv * c.GR * 8;  // jobs a token: a lane's eight channels of K and of V
+  const uint32_t jobs = n * line;          // below 2^31
+  const uint4* K = static_cast<const uint4*>(a.K) + tok0 * (a.kv_stride / 8);
+  const uint4* V = static_cast<const uint4*>(a.V) + tok0 * (a.kv_stride / 8);
+  for (uint32_t base = first - (threadIdx.x & 31); base < jobs; base += stride) {
+    const uint32_t e = base + (threadIdx.x & 31);
     const bool live = e < jobs;
-    const int64_t ec = live ? e : jobs - 1;
-    const int w = (int)(ec & 7);  // word of the group
-    const int64_t grp = ec >> 3;
-    const int g = (int)(grp % c.GR);
-    const int64_t th = grp / c.GR;
-    const int head = (int)(th % c.Hkv);
-    const int64_t t = th / c.Hkv;
-    const int64_t src = ((tok0 + t) * a.kv_stride + (int64_t)head * d + 64 * g) / 8 + w;
+    const uint32_t ec = live ? e : jobs - 1;
+    const uint32_t t = ec / line, x = ec - t * line;  // x: 16-byte piece of the token's row
+    const int w = x & 7, g = (x >> 3) & (c.GR - 1), head = x / (8 * c.GR);
+    const int64_t src = (int64_t)t * (a.kv_stride / 8) + x;
     const uint4 ku = __ldg(K + src), vu = __ldg(V + src);
     uint32_t kp, vp;
     const uint32_t kw = quantize8(ku, kp), vw = quantize8(vu, vp);
@@ -128,8 +132,8 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4AppendArgs a
   }
   if (!a.acc && !a.pos) return;
   const int pos0 = (a.n_tokens ? a.n_tokens[b] : len) - n;
-  for (int64_t e = first; e < (int64_t)n * c.Hkv; e += stride) {
-    const int head = (int)(e / n), t = (int)(e % n);
+  for (uint32_t e = first; e < (uint32_t)n * c.Hkv; e += stride) {
+    const int head = e / n, t = e - head * n;
     const int64_t out = ((int64_t)b * c.Hkv + head) * a.ld + start + t;
     if (a.acc) {
       float sum = 0.f;
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4AppendArgs a
 
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4ReadArgs a) {
   const Kv4Cache& c = a.c;
-  const int b = blockIdx.y, d = c.GR * 64;
+  const int b = blockIdx.y;
   int64_t tok0;
   int n, len;
   bool ok = seq_range(a.cu, a.total, a.max_read, b, tok0, n);
@@ -155,20 +159,16 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4ReadArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, VS_DEVFLAG_BOUNDS);
     return;
   }
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  const int64_t jobs = (int64_t)n * c.Hkv * c.GR * 8;
-  uint4* K = static_cast<uint4*>(a.K);
-  uint4* V = static_cast<uint4*>(a.V);
-  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < jobs; e += stride) {
-    const int w = (int)(e & 7);
-    const int64_t grp = e >> 3;
-    const int g = (int)(grp % c.GR);
-    const int64_t th = grp / c.GR;
-    const int head = (int)(th % c.Hkv);
-    const int64_t t = th / c.Hkv;
+  const uint32_t stride = gridDim.x * blockDim.x;
+  const uint32_t line = c.Hkv * c.GR * 8, jobs = n * line;  // as in the append
+  uint4* K = static_cast<uint4*>(a.K) + tok0 * (a.kv_stride / 8);
+  uint4* V = static_cast<uint4*>(a.V) + tok0 * (a.kv_stride / 8);
+  for (uint32_t e = blockIdx.x * blockDim.x + threadIdx.x; e < jobs; e += stride) {
+    const uint32_t t = e / line, x = e - t * line;
+    const int w = x & 7, g = (x >> 3) & (c.GR - 1), head = x / (8 * c.GR);
     const int slot = start + (int)t, r = slot & 63;
     const uint8_t* page = kv4_page(c, b, slot >> 6, head);
-    const int64_t dst = ((tok0 + t) * a.kv_stride + (int64_t)head * d + 64 * g) / 8 + w;
+    const int64_t dst = (int64_t)t * (a.kv_stride / 8) + x;
     if (!page) {
       atomicOr(a.status, VS_DEVFLAG_BOUNDS);
       continue;

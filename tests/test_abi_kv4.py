@@ -73,7 +73,9 @@ def test_append_and_read_arguments(call):
     assert call(kvs=248) == vs.VS_ERR_INVALID_ARG
     assert call(kvs=260) == vs.VS_ERR_UNSUPPORTED
     assert call(K=_fake(0x10008)) == vs.VS_ERR_UNSUPPORTED
-    assert call(**{"max_new" if call is _append else "max_read": 0}) == vs.VS_ERR_INVALID_ARG
+    most = "max_new" if call is _append else "max_read"
+    assert call(**{most: 0}) == vs.VS_ERR_INVALID_ARG
+    assert call(**{most: 1 << 26}) == vs.VS_ERR_UNSUPPORTED  # 2^26 * 2 * 16 pieces
 
 
 def test_append_arguments():
