@@ -23,64 +23,89 @@ namespace vs {
 
 constexpr int kKv4Threads = 256;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // NaN if either is
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                       *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                       *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ __nv_bfloat162 abs2(uint32_t a) {
+  a &= 0x7fff7fffu;
+  return *reinterpret_cast<__nv_bfloat162*>(&a);
+}
+__device__ __forceinline__ float bf16_at(const uint32_t (&v)[4], int i) {
+  return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+}
+
+// Adding this to x in [0, 2^22) leaves rint(x) in the low bits.
+constexpr float kRound = 12582912.f;  // 1.5 2^23
+constexpr uint32_t kRoundBits = 0x4b400000u;
+
 // Codes of this lane's eight channels and the pair of the group that the
-// eight lanes of an aligned octet hold (the whole warp must call it).
+// eight lanes of an aligned octet hold (the whole warp must call it).  No
+// conversion instructions (their unit is narrow): rounding and integers come
+// from the addition of kRound.
 __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
-  float x[8];
-  unpack8(u, x);
-  float lo = x[0], hi = x[0];
-  bool bad = false;
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+  const uint32_t mn = min2(min2(v[0], v[1]), min2(v[2], v[3]));
+  const uint32_t mx = max2(max2(v[0], v[1]), max2(v[2], v[3])) ^ 0x80008000u;
+  uint32_t ends = min2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));  // min, -max
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const uint32_t bads = __ballot_sync(0xffffffffu, bad);
-  const int lane = threadIdx.x & 31;
-  if ((bads >> (lane & 24)) & 0xffu) {
+  for (int o = 1; o < 8; o <<= 1) ends = min2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+  const float lo = __uint_as_float(ends << 16), hi = -__uint_as_float(ends & 0xffff0000u);
+  if (!(lo > -INFINITY && hi < INFINITY)) {  // also where either is NaN
     pair = 0x7fc07fc0u;
     return 0u;
   }
-  const double lo64 = lo;
   // (hi - lo) / 15 to within 2^-22: the bf16 it rounds to, unless its low half
-  // is next to 0x8000, it is subnormal or hi - lo overflowed
+  // is next to 0x8000 or it is not well inside the normal range
   float range = (hi - lo) * (1.f / 15.f);
   const int low = (int)(__float_as_uint(range) & 0xffffu) - 0x8000;
-  if ((low < 8 && low > -8) || !(range > 1e-30f && range < 1e37f))
-    range = (float)(((double)hi - lo64) / 15.0);
+  const bool normal = range > 1e-30f && range < 1e37f;
+  if ((low < 8 && low > -8) || !normal) range = (float)(((double)hi - (double)lo) / 15.0);
   const __nv_bfloat16 sb = __float2bfloat16_rn(range);
   const float s = __bfloat162float(sb);
-  pair = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
+  pair = (uint32_t)__bfloat16_as_ushort(sb) | (ends << 16);
   if (s == 0.f) return 0u;
-  const float r = 1.f / s;
+  // q = (x - lo) / s, the product corrected once by the remainder: a quotient
+  // that is a whole number and a half comes out as such, and no other does,
+  // for (x - lo) - (n + 1/2) s is a multiple of the smallest unit in the last
+  // place among x, lo and s / 2, hence 0 or above 2^-24 (x - lo) -- unless x
+  // or lo is below 2^-16 of the range (and not 0; 2^-15 is tested).
+  const float tiny = range * (15.f * 0x1p-15f);
+  bool exact = normal && (fabsf(lo) >= tiny || lo == 0.f);
+  const __nv_bfloat162 least = __hmin2(__hmin2(abs2(v[0]), abs2(v[1])), __hmin2(abs2(v[2]), abs2(v[3])));
+  if (!(fminf(__low2float(least), __high2float(least)) >= tiny)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) exact &= fabsf(bf16_at(v, i)) >= tiny || bf16_at(v, i) == 0.f;
+  }
+  const float r = __fdividef(1.f, s);  // to 2^-22
   uint32_t word = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = (x[i] - lo) * r;
-    float n = rintf(q);
-    // near a half (or not a number: x - m or 1 / s overflowed), decide exactly
-    if (!(fabsf(q - n) < 0.4999f)) n = (float)rint(((double)x[i] - lo64) / (double)s);
-    word |= (uint32_t)(int)fminf(fmaxf(n, 0.f), 15.f) << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    const float d = bf16_at(v, i) - lo, q = d * r;
+    const float x = fmaf(fmaf(-q, s, d), r, q) + kRound;  // below 15.1
+    word = word * 16u + __float_as_uint(x);
+  }
+  word -= kRoundBits * 0x11111111u;  // of all eight
+  if (!exact) {  // quotients next to a half, or overflowed, in 64 bits
+    word = 0;
+    for (int i = 7; i >= 0; --i) {
+      const float d = bf16_at(v, i) - lo, q = d * r;
+      float n = (q + kRound) - kRound;
+      if (!normal || !(fabsf(q - n) < 0.4999f))
+        n = (float)rint(fmin(((double)bf16_at(v, i) - (double)lo) / (double)s, 15.0));
+      word = word * 16u + (uint32_t)n;
+    }
   }
   return word;
 }
@@ -105,18 +130,32 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4AppendArgs a
   const uint32_t jobs = n * line;          // below 2^31
   const uint4* K = static_cast<const uint4*>(a.K) + tok0 * (a.kv_stride / 8);
   const uint4* V = static_cast<const uint4*>(a.V) + tok0 * (a.kv_stride / 8);
-  for (uint32_t base = first - (threadIdx.x & 31); base < jobs; base += stride) {
-    const uint32_t e = base + (threadIdx.x & 31);
-    const bool live = e < jobs;
-    const uint32_t ec = live ? e : jobs - 1;
-    const uint32_t t = ec / line, x = ec - t * line;  // x: 16-byte piece of the token's row
-    const int w = x & 7, g = (x >> 3) & (c.GR - 1), head = x / (8 * c.GR);
+  // job e = t line + x is 16-byte piece x of token t's row; both move on by
+  // `stride` jobs without a division
+  const uint32_t dt = stride / line, dx = stride - dt * line;
+  uint32_t t = first / line, x = first - t * line;
+  auto load = [&](uint32_t t, uint32_t x, uint4& k, uint4& v) {
     const int64_t src = (int64_t)t * (a.kv_stride / 8) + x;
-    const uint4 ku = __ldg(K + src), vu = __ldg(V + src);
+    k = __ldg(K + src);
+    v = __ldg(V + src);
+  };
+  uint4 kn = make_uint4(0, 0, 0, 0), vn = kn;  // the next job's, loaded one turn ahead
+  if (first < jobs) load(t, x, kn, vn);
+  for (uint32_t base = first - (threadIdx.x & 31); base < jobs; base += stride) {
+    const bool live = base + (threadIdx.x & 31) < jobs;
+    const uint4 ku = kn, vu = vn;
+    const int slot = start + (int)t;
+    const int w = x & 7, g = (x >> 3) & (c.GR - 1), head = x >> (c.GR == 1 ? 3 : 4);
+    t += dt;
+    x += dx;
+    if (x >= line) {
+      x -= line;
+      ++t;
+    }
+    if (base + stride + (threadIdx.x & 31) < jobs) load(t, x, kn, vn);
     uint32_t kp, vp;
     const uint32_t kw = quantize8(ku, kp), vw = quantize8(vu, vp);
     if (!live) continue;
-    const int slot = start + (int)t;
     uint8_t* page = kv4_page(c, b, slot >> 6, head);
     if (!page) {
       atomicOr(a.status, VS_DEVFLAG_BOUNDS);
@@ -146,6 +185,11 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_kernel(Kv4AppendArgs a
   }
 }
 
+// Code i of a word as a float.
+__device__ __forceinline__ float code(uint32_t word, int i) {
+  return __uint_as_float(((word >> (4 * i)) & 15u) | kRoundBits) - kRound;
+}
+
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4ReadArgs a) {
   const Kv4Cache& c = a.c;
   const int b = blockIdx.y;
@@ -163,9 +207,14 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4ReadArgs a) {
   const uint32_t line = c.Hkv * c.GR * 8, jobs = n * line;  // as in the append
   uint4* K = static_cast<uint4*>(a.K) + tok0 * (a.kv_stride / 8);
   uint4* V = static_cast<uint4*>(a.V) + tok0 * (a.kv_stride / 8);
-  for (uint32_t e = blockIdx.x * blockDim.x + threadIdx.x; e < jobs; e += stride) {
-    const uint32_t t = e / line, x = e - t * line;
-    const int w = x & 7, g = (x >> 3) & (c.GR - 1), head = x / (8 * c.GR);
+  const uint32_t dt = stride / line, dx = stride - dt * line;
+  uint32_t e = blockIdx.x * blockDim.x + threadIdx.x, t = e / line, x = e - t * line;
+  for (; e < jobs; e += stride, t += dt, x += dx) {
+    if (x >= line) {
+      x -= line;
+      ++t;
+    }
+    const int w = x & 7, g = (x >> 3) & (c.GR - 1), head = x >> (c.GR == 1 ? 3 : 4);
     const int slot = start + (int)t, r = slot & 63;
     const uint8_t* page = kv4_page(c, b, slot >> 6, head);
     const int64_t dst = (int64_t)t * (a.kv_stride / 8) + x;
@@ -183,8 +232,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(Kv4ReadArgs a) {
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)  // s n is exact in fp32, so one rounding each: + m, then bf16
-        o[i] = pack2(fmaf((float)((word >> (8 * i)) & 15u), s, m),
-                     fmaf((float)((word >> (8 * i + 4)) & 15u), s, m));
+        o[i] = pack2(fmaf(code(word, 2 * i), s, m), fmaf(code(word, 2 * i + 1), s, m));
       (kv ? V : K)[dst] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
