@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
   __shared__ __align__(8) uint64_t bars[2 * kSlots];  // full, empty
   __shared__ bool s_valid[kSlots];                    // a page of the pool
   __shared__ int s_abort, s_last;
-  __shared__ int s_sum[kDecWarps + 1];
+  __shared__ int s_sum[kDecWarps + 1], s_long[kDecWarps + 1];
   __shared__ int s_start[2];
   __shared__ const float* s_part[kDecWarps];
-  __shared__ float s_fac[kDecWarps][HT], s_sumw[kDecWarps][HT], s_join[2 * HT], s_inv[HT];
+  __shared__ float s_fac[32][HT], s_join[2 * HT], s_inv[HT];
   constexpr int kJoin = (HT * D + 4 * kDecThreads - 1) / (4 * kDecThreads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
@@ -243,12 +243,14 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
   constexpr int kAll = Shape::kThreads;
   const int per = (c.B + kAll - 1) / kAll;
   const int b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
-  int mine = 0;
+  int mine = 0, longest = 0;
   for (int b = b0; b < b1; ++b) {
     int n;
     const bool ok = kv4_len(c, b, n);
     if (blockIdx.x == 0 && !ok) atomicOr(P.status, VS_DEVFLAG_BOUNDS);
-    mine += visible_pages(n, P.window, P.sinks).pages * RPS;
+    const int pages = visible_pages(n, P.window, P.sinks).pages;
+    mine += pages * RPS;
+    longest = max(longest, pages);
   }
   int incl = mine;  // over the lanes, then over the warps
 #pragma unroll
@@ -256,18 +258,38 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     const int x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
-  if (lane == 31) s_sum[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    s_sum[warp] = incl;
+    s_long[warp] = longest;
+  }
   __syncthreads();
   int total = 0, before = incl - mine;
 #pragma unroll
   for (int w = 0; w <= kDecWarps; ++w) {
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
+    longest = max(longest, s_long[w]);
   }
+  // Rows of no more pages than there are warps, and no more rows than CTAs: a
+  // row each, so that nothing is shared.  Else equal ranges of the list.
+  const bool by_row = longest <= kTeams && c.B * RPS <= (int)gridDim.x;
   const int share = max(kDecMinPages, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const int f0 = min((int64_t)blockIdx.x * share, (int64_t)total);
-  const int f1 = min((int64_t)f0 + share, (int64_t)total);
-  {
+  int f0 = min((int64_t)blockIdx.x * share, (int64_t)total);
+  int f1 = min((int64_t)f0 + share, (int64_t)total);
+  if (by_row) {
+    const int b = blockIdx.x / RPS;
+    f0 = f1 = 0;
+    if (b < c.B) {
+      int n;
+      kv4_len(c, b, n);
+      f1 = visible_pages(n, P.window, P.sinks).pages;
+      if (tid == 0) {
+        s_start[0] = b;
+        s_start[1] = (blockIdx.x - b * RPS) * f1;
+      }
+    }
+  } else {
     int at = before;
     if (f0 < f1 && at <= f0 && f0 < at + mine) {
       int b = b0;
@@ -699,22 +721,24 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     // a CTA has at most two shared rows: the one its range starts in and the
     // one it ends in
     float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * kPart;
-    if (tid < HT) {  // the warps' factors for this head
-      float M = -INFINITY, L = 0.f;
-      for (int w = 0; w < kDecWarps; ++w)
-        if (s_part[w]) M = fmaxf(M, s_part[w][HT * D + tid]);
-      const float Mb = M == -INFINITY ? 0.f : M;
-      for (int w = 0; w < kDecWarps; ++w)
-        if (s_part[w]) {
-          const float fw = ex2_approx(s_part[w][HT * D + tid] - Mb);
-          s_fac[w][tid] = fw;
-          L = fmaf(fw, s_part[w][HT * D + HT + tid], L);
+    for (int h = warp; h < HT; h += kDecWarps) {  // the warps' factors for head h, a lane each
+      const float* pw = lane < kDecWarps ? s_part[lane] : nullptr;
+      const float mw = pw ? pw[HT * D + h] : -INFINITY;
+      float M = mw;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float fw = pw ? ex2_approx(mw - (M == -INFINITY ? 0.f : M)) : 0.f;
+      float L = pw ? fw * pw[HT * D + HT + h] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane < kDecWarps) s_fac[lane][h] = fw;
+      if (lane == 0) {
+        if (shared) {
+          out[HT * D + h] = M;
+          out[HT * D + HT + h] = L;
+        } else {
+          finish(h, M, L);
         }
-      if (shared) {
-        out[HT * D + tid] = M;
-        out[HT * D + HT + tid] = L;
-      } else {
-        finish(tid, M, L);
       }
     }
     compute_sync();
@@ -743,34 +767,37 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
           return P.parts + (size_t)(2 * x + ((int64_t)x * share < row0 ? 1 : 0)) * kPart;
         };
         // a warp per head: maximum over the parts, then their factors, in
-        // pieces of kDecWarps parts (s_fac's size), added in the parts' order
+        // pieces of 32 parts, added in the parts' order
         float4 num[kJoin];
 #pragma unroll
         for (int q = 0; q < kJoin; ++q) num[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (tid < HT) s_join[tid] = 0.f;
         for (int h = warp; h < HT; h += kDecWarps) {
           float M = -INFINITY;
           for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HT * D + h));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          if (lane == 0) s_join[HT + h] = M;
+          if (lane == 0) {
+            s_join[HT + h] = M;
+            s_join[h] = 0.f;
+          }
         }
-        for (int x0 = c0; x0 <= c1; x0 += kDecWarps) {
-          const int parts = min(kDecWarps, c1 - x0 + 1);
-          compute_sync();
-          for (int e = tid; e < kDecWarps * HT; e += kDecThreads) {
-            const int x = e / HT, h = e % HT;
-            if (x < parts) {
-              const float M = s_join[HT + h], Mb = M == -INFINITY ? 0.f : M;
-              const float* px = part_of(x0 + x) + HT * D + h;
-              const float fx = ex2_approx(__ldcg(px) - Mb);
-              s_fac[x][h] = fx;
-              s_sumw[x][h] = fx * __ldcg(px + HT);
+        for (int x0 = c0; x0 <= c1; x0 += 32) {
+          const int parts = min(32, c1 - x0 + 1);
+          __syncwarp();
+          for (int h = warp; h < HT; h += kDecWarps) {  // the same warp as above
+            const float M = s_join[HT + h];
+            float fx = 0.f, L = 0.f;
+            if (lane < parts) {
+              const float* px = part_of(x0 + lane) + HT * D + h;
+              fx = ex2_approx(__ldcg(px) - (M == -INFINITY ? 0.f : M));
+              L = fx * __ldcg(px + HT);
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            s_fac[lane][h] = fx;
+            if (lane == 0) s_join[h] += L;
           }
           compute_sync();
-          if (tid < HT)
-            for (int x = 0; x < parts; ++x) s_join[tid] += s_sumw[x][tid];
 #pragma unroll
           for (int q = 0; q < kJoin; ++q) {
             const int e = 4 * (tid + q * kDecThreads);
@@ -781,8 +808,8 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
                      __ldcg(reinterpret_cast<const float4*>(part_of(x0 + x) + e)));
             }
           }
+          compute_sync();
         }
-        compute_sync();
         if (tid < HT) {
           const float M = s_join[HT + tid], L = s_join[tid];
           finish(tid, M, L);
@@ -879,7 +906,8 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
   const int64_t rows = (int64_t)a.c.B * a.c.Hkv * L.HC;
   // no more CTAs than the longest possible list fills
   const int64_t most = rows * (L.slots / kKv4Page);
-  const int64_t want = (most + kDecMinPages - 1) / kDecMinPages;
+  const int64_t by_pages = (most + kDecMinPages - 1) / kDecMinPages;
+  const int64_t want = by_pages > rows ? by_pages : rows;
   const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
   if (L.HT == 8)
     e = a.c.GR == 1 ? launch_decode_impl<1, 1>(P, grid, a.stream)
