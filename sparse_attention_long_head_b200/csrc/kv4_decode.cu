@@ -40,20 +40,18 @@ namespace vs {
 
 // Compute warps (and one more that issues the copies): four warps a scheduler
 // leave 128 registers a thread, enough for 8 query heads a row; the
-// accumulators of 16 need the 255 of two a scheduler.  The warps of a team take
-// a page together, so that fewer of the ring's slots (what 216 KB of shared
-// memory hold) are in use and more are being filled.
+// accumulators of 16 need the 255 of two a scheduler.  Ring slots: what 216 KB
+// of shared memory hold.
 template <int GR, int NT>
 struct DecodeShape {
   static constexpr int kWarps = NT == 1 ? 15 : 7;
-  static constexpr int kTeam = 1;
-  static constexpr int kTeams = kWarps / kTeam;
   static constexpr int kSlots = 48 / GR;
   static constexpr int kCompute = 32 * kWarps;  // compute threads
   static constexpr int kThreads = kCompute + 32;
   static constexpr int kFetch = 4;  // pages issued together
-  static_assert(kSlots > kTeams + kFetch && 32 % kFetch == 0, "see the copying warp");
+  static_assert(kSlots > kWarps + kFetch && 32 % kFetch == 0, "see the copying warp");
 };
+
 // The weights carry 2^kShift: V steps s from 2^-40 (below, the products with
 // codes of 2^-133 lose bits) to 2^60 (above, sums over long rows overflow).
 constexpr float kShift = 48.f;
@@ -62,7 +60,7 @@ constexpr int kDecMinPages = 8;  // per CTA, where the list is short
 // Workspace: status and tickets (zeroed by the call), then parts, the rows'
 // log2-sum-exp and the scores (the last two only where weights are asked for).
 struct DecodeLayout {
-  int HT = 0;       // query heads a row: 8 or 16
+  int HT = 0;       // query heads a row: 4, 8 or 16
   int HC = 1;       // rows per KV head
   int Gp = 0;       // scores per slot and KV head (G rounded up to even)
   int64_t slots = 0;
@@ -72,7 +70,7 @@ struct DecodeLayout {
   static DecodeLayout make(int B, int Hq, int Hkv, int d, int max_len, bool weights, int sms) {
     DecodeLayout L;
     const int G = Hq / Hkv;
-    L.HT = G <= 8 ? 8 : 16;
+    L.HT = G <= 4 ? 4 : G <= 8 ? 8 : 16;
     L.HC = (G + L.HT - 1) / L.HT;
     L.Gp = (G + 1) / 2 * 2;
     L.slots = (int64_t)ceil_div(max_len, kKv4Page) * kKv4Page;
@@ -130,6 +128,28 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Waits until *count > i, with the limits of mbar_wait.
+__device__ __forceinline__ bool wait_count(const int* count, int i, const WaitCtx& w) {
+  auto now = [&]() {
+    int x;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(x) : "r"(smem_u32(count)) : "memory");
+    return x;
+  };
+  if (now() > i) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (now() > i) return true;
+    if ((it & 255u) == 0) {
+      if (*w.abort_cta) return false;
+      if (globaltimer_ns() - t0 > w.limit_ns) {
+        atomicOr(w.status, VS_DEVFLAG_TIMEOUT);
+        *w.abort_cta = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // D += A B, one m16n8k16 bf16 tile.
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -138,6 +158,16 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two 16 x 16 matrices of bytes, transposed; lane i gives the address of row i
+// (mod 16) of matrix i / 16.  Lane (gid, tig) gets of matrix m, in r[2 m] and
+// r[2 m + 1], the bytes of rows 4 tig .. 4 tig + 3 in columns gid and gid + 8.
+__device__ __forceinline__ void load_bytes_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // Transposes an 8 x 8 matrix of 16-bit values held one row per four lanes.
@@ -205,29 +235,41 @@ __device__ __forceinline__ void cursor_add(const DecodeParams& P, Cursor& q, int
   }
 }
 
-template <int GR, int NT>
+// A row's query heads are the 8 NT columns of the MMAs.  PACK (up to four
+// heads): columns 0..3 and 4..7 are the same heads over two tiles of slots, as
+// two softmax states that the merge joins, so that one set of scores, weights
+// and pairs covers 32 slots.  Per 16 slots that saves some 20% of the
+// instructions, which is what bounds the loop: 4 x 128K slots at 4 query heads
+// a KV head and d = 128 take 125 us packed and 131 us not.
+template <int GR, int NT, bool PACK>
 __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     kv4_decode_kernel(const DecodeParams P) {
+  static_assert(!PACK || NT == 1, "packing is for few heads");
   constexpr int D = 64 * GR, HT = 8 * NT;
+  constexpr int HR = PACK ? 4 : HT;  // query heads a row
+  constexpr int kSub = HT / HR;      // softmax states of a head in a warp
   using Shape = DecodeShape<GR, NT>;
   constexpr int kDecWarps = Shape::kWarps, kSlots = Shape::kSlots, kDecThreads = Shape::kCompute;
-  constexpr int kTeam = Shape::kTeam, kTeams = Shape::kTeams, kFetch = Shape::kFetch;
-  // floats of a warp's part of a row: O [HT][D], m and l [HT]
-  constexpr int kPart = HT * (D + 2);
+  constexpr int kFetch = Shape::kFetch;
+  // floats of a warp's part of a row (O [HT][D], m and l [HT]) and of a CTA's
+  constexpr int kWarpPart = HT * (D + 2), kPart = HR * (D + 2);
   constexpr int kChunk = GR * kKv4GroupBytes;
-  constexpr int TT = 2;  // tiles a step: their chains of dependent instructions overlap
+  // tiles of 16 slots a step (their chains of dependent instructions overlap),
+  // and sets of scores
+  constexpr int TT = PACK ? 4 : 2, U = TT / kSub;
   extern __shared__ __align__(128) uint8_t smem[];
-  // ring [slot][kChunk]; the slot of a team's last page of a row also carries
-  // its warps' parts to the merge
-  static_assert(sizeof(float) * kTeam * kPart <= kChunk, "the parts fit a slot");
+  // ring [slot][kChunk]; the slot of a warp's last page of a row also carries
+  // its part to the merge
+  static_assert(sizeof(float) * kWarpPart <= kChunk, "a part fits a slot");
   __shared__ __align__(8) uint64_t bars[2 * kSlots];  // full, empty
   __shared__ bool s_valid[kSlots];                    // a page of the pool
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort, s_last, s_issued;  // s_issued: pages copied or on their way
   __shared__ int s_sum[kDecWarps + 1], s_long[kDecWarps + 1];
   __shared__ int s_start[2];
   __shared__ const float* s_part[kDecWarps];
-  __shared__ float s_fac[32][HT], s_join[2 * HT], s_inv[HT];
-  constexpr int kJoin = (HT * D + 4 * kDecThreads - 1) / (4 * kDecThreads);
+  static_assert(kDecWarps * kSub <= 32, "a lane each in the merge");
+  __shared__ float s_fac[32][HR], s_join[2 * HR], s_inv[HR];
+  constexpr int kJoin = (HR * D + 4 * kDecThreads - 1) / (4 * kDecThreads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const Kv4Cache& c = P.c;
@@ -235,7 +277,8 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
 
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(smem_u32(&bars[i]), i < kSlots ? 1 : kTeam);
+    s_issued = 0;
+    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(smem_u32(&bars[i]), 1);
     fence_mbar_init();
   }
   // the list's length, and where this CTA's range starts: thread i sums a
@@ -273,7 +316,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
   }
   // Rows of no more pages than there are warps, and no more rows than CTAs: a
   // row each, so that nothing is shared.  Else equal ranges of the list.
-  const bool by_row = longest <= kTeams && c.B * RPS <= (int)gridDim.x;
+  const bool by_row = longest <= kDecWarps && c.B * RPS <= (int)gridDim.x;
   const int share = max(kDecMinPages, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   int f0 = min((int64_t)blockIdx.x * share, (int64_t)total);
   int f1 = min((int64_t)f0 + share, (int64_t)total);
@@ -325,7 +368,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
   seg.hc = s_start[1] / seg.v.pages % P.HC;
   const int count = f1 - f0;
   const WaitCtx wc{P.wait_limit_ns, P.status, &s_abort};
-  // Page i of the CTA's range goes to slot i mod kSlots and to team i mod kTeams.
+  // Page i of the CTA's range goes to slot i mod kSlots and compute warp i mod kDecWarps.
   auto full = [&](int slot) { return smem_u32(&bars[slot]); };
   auto empty = [&](int slot) { return smem_u32(&bars[kSlots + slot]); };
 
@@ -333,9 +376,9 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     // ------------------------------------------------------- copies
     // Lane q looks up the pages q, q + 32, ...; the whole warp waits for the
     // slots of kFetch pages, one after the other, and their lanes issue.  A
-    // slot that a merge holds back is among its row's last kTeams pages; all
+    // slot that a merge holds back is among its row's last kDecWarps pages; all
     // pages of that row are issued by then, for the ring has more slots than
-    // kTeams + kFetch.
+    // kDecWarps + kFetch.
     auto source = [&]() {
       return kv4_page(c, seg.b, seg.k < seg.v.first ? seg.k : seg.k + seg.v.gap, seg.head);
     };
@@ -378,6 +421,10 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
           }
         }
         __syncwarp();
+        if (lane == 0)
+          asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&s_issued)),
+                       "r"(i + kFetch)
+                       : "memory");
       }
       src = next;
     }
@@ -389,8 +436,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     return;
   }
 
-  const int team = warp / kTeam, member = warp % kTeam;
-  int slot = team;  // of the team's next page
+  int slot = warp;  // of this warp's next page
   uint32_t phase = 0;
   auto compute_sync = [&]() {  // the compute warps, each converged
     __syncwarp();
@@ -404,11 +450,11 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     int n;
     kv4_len(c, seg.b, n);
     const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
-    const int heads = min(HT, P.G - hc * HT);
-    const int h0 = head * P.G + hc * HT;  // first query head of the row
+    const int heads = min(HR, P.G - hc * HR);
+    const int h0 = head * P.G + hc * HR;  // first query head of the row
 
-    // Q as the B operand of S^T = K Q^T: head gid, channels in the order the
-    // words' codes give, scaled by f = 2^(field - 127), odd codes' by f / 16.
+    // Q as the B operand of S^T = K Q^T: head gid (mod HR), channels in the
+    // order the words' codes give, scaled by f = 2^(field - 127), odd codes' by f / 16.
     // For this lane's heads: the groups' sums of q, in the units f 2^-133 of
     // the scores, and what takes scores from these units to base 2.
     uint32_t qf[NT][GR][2][4];
@@ -421,9 +467,10 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           uint4 u = make_uint4(0, 0, 0, 0);
-          if (8 * nt + gid < heads)
+          const int h = PACK ? gid & 3 : 8 * nt + gid;
+          if (h < heads)
             u = __ldg(reinterpret_cast<const uint4*>(P.Q + (int64_t)seg.b * P.q_stride +
-                                                     (int64_t)(h0 + 8 * nt + gid) * D + 64 * g +
+                                                     (int64_t)(h0 + h) * D + 64 * g +
                                                      8 * (2 * tig + w)));
           qf[nt][g][w][0] = __byte_perm(u.x, u.z, 0x5410);  // channels 0, 4
           qf[nt][g][w][1] = __byte_perm(u.x, u.z, 0x7632);  // 1, 5
@@ -478,14 +525,19 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = nb[nt][0] = nb[nt][1] = 0.f;
     }
-    int last = -1;  // slot of the team's last page of the row so far
-    // the team's pages of the row
-    for (int i = at + (team + kTeams - at % kTeams) % kTeams; i < at + (k1 - k0); i += kTeams) {
+    int last = -1;  // slot of this warp's last page of the row so far
+    // this warp's pages of the row
+    for (int i = at + (warp + kDecWarps - at % kDecWarps) % kDecWarps; i < at + (k1 - k0);
+         i += kDecWarps) {
       const int k = k0 + (i - at);
       if (last >= 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(last));
       }
+      // The slot's previous page belongs to another warp.  Until this page has
+      // been issued, hence the previous one used up, the barrier may be a phase
+      // behind, and the parity of this page's would read as completed.
+      if (ok) ok = wait_count(&s_issued, i, wc);
       if (ok) ok = mbar_wait(full(slot), phase, wc);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {  // a copy may still be on its way into the slot
@@ -493,7 +545,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
         continue;
       }
       last = slot;
-      if ((slot += kTeams) >= kSlots) {
+      if ((slot += kDecWarps) >= kSlots) {
         slot -= kSlots;
         phase ^= 1u;
       }
@@ -506,71 +558,81 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
 
       auto hidden = [&](int t) { return t >= n || (t < lo_slot && t >= P.sinks); };
 
-      // Tiles of 16 slots; row x of a tile is its slot perm(x), so that the
-      // lanes of one load touch all banks for both K (rows gid) and V (rows
-      // 2 tig, 2 tig + 1).  One tile's code, looped: a short row runs it from
-      // a cold instruction cache.
-      auto perm = [](int x) { return x ^ ((x >> 2) & 1); };
-      const int ra = perm(gid);
+      // TT tiles of 16 slots a step, looped where a page has more: a short row
+      // runs the code from a cold instruction cache.
+      const int mine = PACK ? 16 * (tig >> 1) + gid : gid;  // slot of this lane's row gid
+      const int vrow = 2 * ((lane >> 2) & 3) + ((lane >> 1) & 1) + 8 * (lane & 1);
       const int tiles = min(4, (n - t0 + 15) / 16);
 #pragma unroll 1
-      for (int tl = TT * member; tl < tiles; tl += TT * kTeam) {
-        const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, 16 * tl + ra) + 8 * tig;
-        const uint8_t* va = pg + kv4_code_off(GR, 1, 0, 16 * tl + perm(2 * tig)) + 4 * gid;
-        const uint8_t* vb = pg + kv4_code_off(GR, 1, 0, 16 * tl + perm(2 * tig + 1)) + 4 * gid;
-        const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, 16 * tl + ra);
-        float sc[TT][NT][4];
+      for (int tl = 0; tl < tiles; tl += TT) {
+        const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, 16 * tl + gid) + 8 * tig;
+        const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, 16 * tl + mine);
+        // rows of the byte matrices: slots in the order that makes bytes 0 and
+        // 2 of a register slots 2 tig, 2 tig + 1, and bytes 1 and 3 those + 8
+        const uint32_t vc =
+            smem_u32(pg + kv4_code_off(GR, 1, 0, 16 * tl + vrow)) + 16 * (lane >> 4);
+        float sc[U][NT][4];
 #pragma unroll
         for (int g = 0; g < GR; ++g)
 #pragma unroll
-        for (int u = 0; u < TT; ++u) {
-          const uint2 wa = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes + 512 * u);
-          const uint2 wb = *reinterpret_cast<const uint2*>(kc + g * kKv4Codes + 512 * u + 256);
-          const uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * u);
-          const uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * u + 32);
-          const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
-          const float sa = kv4_step(pa), sb = kv4_step(pb);
-          const float ma = kv4_min(pa), mb = kv4_min(pb);
+          for (int u = 0; u < U; ++u) {
+            const uint32_t pa =
+                *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * kSub * u);
+            const uint32_t pb =
+                *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * kSub * u + 32);
+            const float sa = kv4_step(pa), sb = kv4_step(pb);
+            const float ma = kv4_min(pa), mb = kv4_min(pb);
+            float cacc[kSub][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float cacc[4];
-            mma_bf16_first(cacc, codes_lo(wa.x), codes_lo(wb.x), codes_hi(wa.x), codes_hi(wb.x),
-                           qf[nt][g][0][0], qf[nt][g][0][1]);
-            mma_bf16(cacc, codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb),
-                     qf[nt][g][0][2], qf[nt][g][0][3]);
-            mma_bf16(cacc, codes_lo(wa.y), codes_lo(wb.y), codes_hi(wa.y), codes_hi(wb.y),
-                     qf[nt][g][1][0], qf[nt][g][1][1]);
-            mma_bf16(cacc, codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb),
-                     qf[nt][g][1][2], qf[nt][g][1][3]);
+            for (int v = 0; v < kSub; ++v) {
+              const uint8_t* kt = kc + g * kKv4Codes + 512 * (kSub * u + v);
+              const uint2 wa = *reinterpret_cast<const uint2*>(kt);
+              const uint2 wb = *reinterpret_cast<const uint2*>(kt + 256);
+              const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_bf16_first(cacc[v][nt], codes_lo(wa.x), codes_lo(wb.x), codes_hi(wa.x),
+                               codes_hi(wb.x), qf[nt][g][0][0], qf[nt][g][0][1]);
+                mma_bf16(cacc[v][nt], codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb),
+                         qf[nt][g][0][2], qf[nt][g][0][3]);
+                mma_bf16(cacc[v][nt], codes_lo(wa.y), codes_lo(wb.y), codes_hi(wa.y),
+                         codes_hi(wb.y), qf[nt][g][1][0], qf[nt][g][1][1]);
+                mma_bf16(cacc[v][nt], codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb),
+                         qf[nt][g][1][2], qf[nt][g][1][3]);
+              }
+            }
             // q.k = sum_g s (q.n) + m (q.1)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float mm = x < 2 ? ma : mb, ss = x < 2 ? sa : sb, qq = qs[nt][g][x & 1];
-              sc[u][nt][x] = fmaf(ss, cacc[x], g == 0 ? mm * qq : fmaf(mm, qq, sc[u][nt][x]));
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float mm = x < 2 ? ma : mb, ss = x < 2 ? sa : sb, qq = qs[nt][g][x & 1];
+                const float qn = kSub == 2 && tig >= 2 ? cacc[kSub - 1][nt][x] : cacc[0][nt][x];
+                sc[u][nt][x] = fmaf(ss, qn, g == 0 ? mm * qq : fmaf(mm, qq, sc[u][nt][x]));
+              }
           }
-        }
-        const int ta = t0 + 16 * tl + ra;  // slot of row gid of the first tile
+        const int ta = t0 + 16 * tl + mine;  // slot of this lane's row gid in set 0
         if (!whole) {
 #pragma unroll
-          for (int u = 0; u < TT; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              if (hidden(ta + 16 * u)) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
-              if (hidden(ta + 16 * u + 8)) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
+              if (hidden(ta + 16 * kSub * u)) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
+              if (hidden(ta + 16 * kSub * u + 8)) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
             }
         }
         if (P.score) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int hh = hc * HT + 8 * nt + 2 * tig;
+            const int hh = hc * HR + (PACK ? 2 * (tig & 1) : 8 * nt + 2 * tig);
             if (hh < P.Gp) {
               float* dst = P.score + (((int64_t)seg.b * c.Hkv + head) * P.slots + ta) * P.Gp + hh;
 #pragma unroll
-              for (int y = 0; y < 2 * TT; ++y)
-                *reinterpret_cast<float2*>(dst + 8 * y * P.Gp) =
-                    make_float2(sc[y / 2][nt][2 * (y & 1)] * sl[nt][0],
-                                sc[y / 2][nt][2 * (y & 1) + 1] * sl[nt][1]);
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  *reinterpret_cast<float2*>(dst + (16 * kSub * u + 8 * y) * P.Gp) = make_float2(
+                      sc[u][nt][2 * y] * sl[nt][0], sc[u][nt][2 * y + 1] * sl[nt][1]);
             }
           }
         }
@@ -585,7 +647,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
           for (int y = 0; y < 2; ++y) {
             float x = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < TT; ++u) x = fmax3(x, sc[u][nt][y], sc[u][nt][y + 2]);
+            for (int u = 0; u < U; ++u) x = fmax3(x, sc[u][nt][y], sc[u][nt][y + 2]);
             mx[nt][y] = x * sl[nt][y];
             need |= mx[nt][y] > m[nt][y] + 8.f;
           }
@@ -615,9 +677,9 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
               }
             }
         }
-        float p[TT][NT][4];
+        float p[U][NT][4];
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -625,49 +687,53 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
               p[u][nt][x] = ex2_approx(fmaf(sc[u][nt][x], sl[nt][x & 1], nb[nt][x & 1]));
               l[nt][x & 1] += p[u][nt][x];
             }
+        const uint32_t first_half = gid < 4 ? ~0u : 0u;  // columns of a pack's first tile
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int g = 0; g < GR; ++g) {
-          uint32_t pa = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * u);
-          uint32_t pb = *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * u + 32);
-          if (!whole) {  // 0 * NaN of a slot never written
-            if (hidden(ta + 16 * u)) pa = 0;
-            if (hidden(ta + 16 * u + 8)) pb = 0;
-          }
-          const float sa = kv4_step(pa), sb = kv4_step(pb);
-          const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
-          uint32_t bf[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            bf[nt][0] = transpose8(pack_bf16x2(p[u][nt][0] * sa, p[u][nt][1] * sa));
-            bf[nt][1] = transpose8(pack_bf16x2(p[u][nt][2] * sb, p[u][nt][3] * sb));
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              r[nt][g][y] = fmaf(p[u][nt][y], ca, fmaf(p[u][nt][y + 2], cb, r[nt][g][y]));
-          }
-          // V^T as the A operand: channel rows of word gid, slots in pairs
-          const uint32_t v0 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes + 512 * u);
-          const uint32_t v1 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes + 512 * u);
-          const uint32_t v2 = *reinterpret_cast<const uint32_t*>(va + g * kKv4Codes + 512 * u + 256);
-          const uint32_t v3 = *reinterpret_cast<const uint32_t*>(vb + g * kKv4Codes + 512 * u + 256);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t x = __byte_perm(v0, v1, hf ? 0x7632 : 0x5410);
-            const uint32_t y = __byte_perm(v2, v3, hf ? 0x7632 : 0x5410);
-            const uint32_t x8 = x >> 8, y8 = y >> 8;
+          for (int g = 0; g < GR; ++g) {
+            uint32_t pa =
+                *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * kSub * u);
+            uint32_t pb =
+                *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * kSub * u + 32);
+            if (!whole) {  // 0 * NaN of a slot never written
+              if (hidden(ta + 16 * kSub * u)) pa = 0;
+              if (hidden(ta + 16 * kSub * u + 8)) pb = 0;
+            }
+            const float sa = kv4_step(pa), sb = kv4_step(pb);
+            const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
+            uint32_t bf[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float(&oa)[4] = o[nt][g][2 * hf], (&ob)[4] = o[nt][g][2 * hf + 1];
-              mma_bf16(oa, codes_lo(x), codes_hi(x), codes_lo(y), codes_hi(y), bf[nt][0],
-                       bf[nt][1]);
-              mma_bf16(ob, codes_lo(x8), codes_hi(x8), codes_lo(y8), codes_hi(y8), bf[nt][0],
-                       bf[nt][1]);
-              mma_bf16(oa, kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
-              mma_bf16(ob, kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
+              bf[nt][0] = transpose8(pack_bf16x2(p[u][nt][0] * sa, p[u][nt][1] * sa));
+              bf[nt][1] = transpose8(pack_bf16x2(p[u][nt][2] * sb, p[u][nt][3] * sb));
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                r[nt][g][y] = fmaf(p[u][nt][y], ca, fmaf(p[u][nt][y + 2], cb, r[nt][g][y]));
             }
+            // V^T as the A operand: a register is one tile of 16 channels, the
+            // low codes of its bytes in rows 0..7, the high ones in rows 8..15
+#pragma unroll
+            for (int v = 0; v < kSub; ++v) {
+              const uint32_t keep = v == 0 ? first_half : ~first_half;
+              uint32_t x[4];
+              load_bytes_t(x, vc + g * kKv4Codes + 512 * (kSub * u + v));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t b0 = PACK ? bf[nt][0] & keep : bf[nt][0];
+                const uint32_t b1 = PACK ? bf[nt][1] & keep : bf[nt][1];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  mma_bf16(o[nt][g][j], codes_lo(x[j]), codes_hi(x[j]), codes_lo(x[j] >> 8),
+                           codes_hi(x[j] >> 8), b0, b1);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_bf16(o[nt][g][j], kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
           }
-        }
       }
     }
     // ------------------------------------------------------ merge the warps
@@ -686,10 +752,10 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
       *reinterpret_cast<uint2*>(P.O + (int64_t)seg.b * P.q_stride + (int64_t)h0 * D + e) =
           make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
     };
-    compute_sync();  // the other warp of the team may still read the slot
+    __syncwarp();
     float* part = nullptr;
     if (last >= 0) {
-      part = reinterpret_cast<float*>(smem + last * kChunk) + member * kPart;
+      part = reinterpret_cast<float*>(smem + last * kChunk);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -709,7 +775,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
             for (int s = 4; s < 32; s <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, s);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float2*>(part + h * D + 64 * g + 8 * gid + 2 * j) = make_float2(
+              *reinterpret_cast<float2*>(part + h * D + 64 * g + 16 * j + 2 * gid) = make_float2(
                   fmaf(o[nt][g][j][y] * 0x1p100f, 0x1p33f, rs),
                   fmaf(o[nt][g][j][y + 2] * 0x1p100f, 0x1p29f, rs));  // odd codes: 16 n
           }
@@ -721,33 +787,38 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     // a CTA has at most two shared rows: the one its range starts in and the
     // one it ends in
     float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * kPart;
-    for (int h = warp; h < HT; h += kDecWarps) {  // the warps' factors for head h, a lane each
-      const float* pw = lane < kDecWarps ? s_part[lane] : nullptr;
-      const float mw = pw ? pw[HT * D + h] : -INFINITY;
+    for (int h = warp; h < HR; h += kDecWarps) {  // the factors of head h's states, a lane each
+      const float* pw = lane < kDecWarps * kSub ? s_part[lane / kSub] : nullptr;
+      const int col = h + HR * (lane % kSub);
+      const float mw = pw ? pw[HT * D + col] : -INFINITY;
       float M = mw;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       const float fw = pw ? ex2_approx(mw - (M == -INFINITY ? 0.f : M)) : 0.f;
-      float L = pw ? fw * pw[HT * D + HT + h] : 0.f;
+      float L = pw ? fw * pw[HT * D + HT + col] : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane < kDecWarps) s_fac[lane][h] = fw;
+      s_fac[lane][h] = fw;
       if (lane == 0) {
         if (shared) {
-          out[HT * D + h] = M;
-          out[HT * D + HT + h] = L;
+          out[HR * D + h] = M;
+          out[HR * D + HR + h] = L;
         } else {
           finish(h, M, L);
         }
       }
     }
     compute_sync();
-    for (int e = 4 * tid; e < HT * D; e += 4 * kDecThreads) {
+    for (int e = 4 * tid; e < HR * D; e += 4 * kDecThreads) {
       const int h = e / D;
       float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = 0; w < kDecWarps; ++w)
-        if (s_part[w])
-          axpy(num, s_fac[w][h], *reinterpret_cast<const float4*>(s_part[w] + e));
+        if (s_part[w]) {
+#pragma unroll
+          for (int v = 0; v < kSub; ++v)
+            axpy(num, s_fac[w * kSub + v][h],
+                 *reinterpret_cast<const float4*>(s_part[w] + v * HR * D + e));
+        }
       if (shared) *reinterpret_cast<float4*>(out + e) = num;
       else store(e, num);
     }
@@ -771,26 +842,26 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
         float4 num[kJoin];
 #pragma unroll
         for (int q = 0; q < kJoin; ++q) num[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int h = warp; h < HT; h += kDecWarps) {
+        for (int h = warp; h < HR; h += kDecWarps) {
           float M = -INFINITY;
-          for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HT * D + h));
+          for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HR * D + h));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
           if (lane == 0) {
-            s_join[HT + h] = M;
+            s_join[HR + h] = M;
             s_join[h] = 0.f;
           }
         }
         for (int x0 = c0; x0 <= c1; x0 += 32) {
           const int parts = min(32, c1 - x0 + 1);
           __syncwarp();
-          for (int h = warp; h < HT; h += kDecWarps) {  // the same warp as above
-            const float M = s_join[HT + h];
+          for (int h = warp; h < HR; h += kDecWarps) {  // the same warp as above
+            const float M = s_join[HR + h];
             float fx = 0.f, L = 0.f;
             if (lane < parts) {
-              const float* px = part_of(x0 + lane) + HT * D + h;
+              const float* px = part_of(x0 + lane) + HR * D + h;
               fx = ex2_approx(__ldcg(px) - (M == -INFINITY ? 0.f : M));
-              L = fx * __ldcg(px + HT);
+              L = fx * __ldcg(px + HR);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -801,7 +872,7 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kJoin; ++q) {
             const int e = 4 * (tid + q * kDecThreads);
-            if (e < HT * D) {
+            if (e < HR * D) {
 #pragma unroll 4
               for (int x = 0; x < parts; ++x)
                 axpy(num[q], s_fac[x][e / D],
@@ -810,15 +881,15 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
           }
           compute_sync();
         }
-        if (tid < HT) {
-          const float M = s_join[HT + tid], L = s_join[tid];
+        if (tid < HR) {
+          const float M = s_join[HR + tid], L = s_join[tid];
           finish(tid, M, L);
         }
         compute_sync();
 #pragma unroll
         for (int q = 0; q < kJoin; ++q) {
           const int e = 4 * (tid + q * kDecThreads);
-          if (e < HT * D) store(e, num[q]);
+          if (e < HR * D) store(e, num[q]);
         }
       }
     }
@@ -864,9 +935,9 @@ size_t kv4_decode_ws_bytes(int B, int Hq, int Hkv, int d, int max_len, bool weig
   return DecodeLayout::make(B, Hq, Hkv, d, max_len, weights, device_sm_count()).total;
 }
 
-template <int GR, int NT>
+template <int GR, int NT, bool PACK>
 static cudaError_t launch_decode_impl(const DecodeParams& P, int grid, cudaStream_t stream) {
-  auto kern = kv4_decode_kernel<GR, NT>;
+  auto kern = kv4_decode_kernel<GR, NT, PACK>;
   constexpr int smem =
       DecodeShape<GR, NT>::kSlots * GR * kKv4GroupBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -909,12 +980,15 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
   const int64_t by_pages = (most + kDecMinPages - 1) / kDecMinPages;
   const int64_t want = by_pages > rows ? by_pages : rows;
   const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
-  if (L.HT == 8)
-    e = a.c.GR == 1 ? launch_decode_impl<1, 1>(P, grid, a.stream)
-                    : launch_decode_impl<2, 1>(P, grid, a.stream);
+  if (L.HT == 4)
+    e = a.c.GR == 1 ? launch_decode_impl<1, 1, true>(P, grid, a.stream)
+                    : launch_decode_impl<2, 1, true>(P, grid, a.stream);
+  else if (L.HT == 8)
+    e = a.c.GR == 1 ? launch_decode_impl<1, 1, false>(P, grid, a.stream)
+                    : launch_decode_impl<2, 1, false>(P, grid, a.stream);
   else
-    e = a.c.GR == 1 ? launch_decode_impl<1, 2>(P, grid, a.stream)
-                    : launch_decode_impl<2, 2>(P, grid, a.stream);
+    e = a.c.GR == 1 ? launch_decode_impl<1, 2, false>(P, grid, a.stream)
+                    : launch_decode_impl<2, 2, false>(P, grid, a.stream);
   if (e != cudaSuccess || !a.acc_out) return e;
   const int64_t per_row = (L.slots + 255) / 256;
   const int64_t cap = ceil_div(16LL * sms, a.c.B * a.c.Hkv);

@@ -292,6 +292,33 @@ def test_decode_split_rows(lens, Hq, Hkv, d, window, cuda_device):
         assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(acc, acc2)
 
 
+@pytest.mark.parametrize("Hq,d,weights", [(4, 128, False), (4, 128, True), (8, 128, False), (4, 64, False), (16, 128, False)])
+def test_decode_same_bits_from_cold_and_warm_caches(Hq, d, weights, cuda_device):
+    """Pages that come from memory arrive late and out of order; the result does not depend on it."""
+    n = 60000
+    gen = torch.Generator("cuda").manual_seed(Hq + d)
+    pages = 4 * (n // 64 + 1)
+    pool = torch.randint(0, 256, (pages, 2, d // 64 * 4608), dtype=torch.uint8, device="cuda", generator=gen)
+    pool[..., d // 64 * 4096:].view(torch.bfloat16).copy_(
+        torch.tensor([0.25, -2.0], device="cuda").repeat(d // 64 * 128))
+    table = torch.randperm(pages, device="cuda", generator=gen).to(torch.int32).view(4, -1)
+    lens = _ints([n, n - 777, n // 2, n - 64])
+    Q = torch.randn((4, Hq * 2, d), device="cuda", generator=gen).bfloat16()
+    acc = torch.zeros((4, 2, n), device="cuda") if weights else None
+    ws = vs.workspace(vs.vs_kv4_decode_workspace_size(4, Hq * 2, 2, d, n, weights))
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(60):
+        O, lse = torch.empty_like(Q), torch.empty((Hq * 2, 4), device="cuda")
+        if i % 4:
+            flush.fill_(i)
+        vs.vs_kv4_decode_attn_fwd(Q, pool, table, lens, n, O, lse, ws, acc_out=acc)
+        now = [O, lse] + ([acc.clone()] if weights else [])
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(now, first)), i
+    assert vs.vs_read_device_status(ws) == (vs.VS_OK, 0)
+
+
 def test_decode_many_short_sequences(cuda_device):
     rng = np.random.default_rng(8)
     lens = [int(x) for x in rng.integers(0, 130, 700)]
