@@ -38,17 +38,19 @@
 
 namespace vs {
 
-// Compute warps (and one more that issues the copies): four warps a scheduler
-// leave 128 registers a thread, enough for 8 query heads a row; the
-// accumulators of 16 need the 255 of two a scheduler.  Ring slots: what 216 KB
-// of shared memory hold.
+// Compute warps, and one more that issues the copies.  11 and 7 of them leave
+// 168 and 255 registers a thread (three and two warps a scheduler), which the
+// accumulators of 8 and 16 query heads need, and leave enough of the ring's
+// slots (what 216 KB of shared memory hold) to be filled while a page a warp is
+// in use: 4 x 128K slots take 112 us with 11 warps, 120 with 14 at 128
+// registers, 118 with 10.
 template <int GR, int NT>
 struct DecodeShape {
-  static constexpr int kWarps = NT == 1 ? 15 : 7;
+  static constexpr int kWarps = NT == 1 ? 11 : 7;
   static constexpr int kSlots = 48 / GR;
   static constexpr int kCompute = 32 * kWarps;  // compute threads
   static constexpr int kThreads = kCompute + 32;
-  static constexpr int kFetch = 4;  // pages issued together
+  static constexpr int kFetch = 8;  // pages issued together
   static_assert(kSlots > kWarps + kFetch && 32 % kFetch == 0, "see the copying warp");
 };
 
