@@ -23,14 +23,15 @@
 // one KV head) the tensor rate is far from the bound, and operands made in
 // registers go straight in, without a trip through shared or tensor memory.
 //
-// One CTA of 12 warps per SM.  All visible pages of all (sequence, KV head)
-// rows form one list, cut into equal ranges, one per CTA; the pages of a
-// range go round the warps.  Each warp streams its pages (one contiguous bulk
-// copy each) through its own ring of two and keeps its own online softmax;
-// the warps of a CTA merge at the end of a row.  A row that several CTAs share
-// leaves one fp32 part per CTA, and the CTA that arrives last joins them in
-// their order, so results do not depend on the timing.  No CTA waits for
-// another.
+// One CTA per SM.  All visible pages of all (sequence, KV head) rows form one
+// list, cut into equal ranges, one per CTA, and these into one per warp.  A warp
+// streams its pages (one contiguous bulk copy each) through two slots of its
+// own and keeps its own online softmax; it writes the O of rows that lie
+// wholly in its range and leaves an fp32 part of the others (at most two: the
+// first and the last).  No warp waits for another before its range is done.
+// Then the CTA joins its warps' parts row by row; a row that several CTAs share
+// leaves one part per CTA, and the CTA that arrives last joins them in their
+// order, so results do not depend on the timing.  No CTA waits for another.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -38,29 +39,24 @@
 
 namespace vs {
 
-// Compute warps, and one more that issues the copies.  11 and 7 of them leave
-// 168 and 255 registers a thread (three and two warps a scheduler), which the
-// accumulators of 8 and 16 query heads need, and leave enough of the ring's
-// slots (what 216 KB of shared memory hold) to be filled while a page a warp is
-// in use: 4 x 128K slots take 112 us with 11 warps, 120 with 14 at 128
-// registers, 118 with 10.
-template <int GR, int NT>
+// 12 and 8 warps leave 168 and 255 registers a thread (three and two warps a
+// scheduler), which the accumulators of 8 and 16 query heads need.  Two page
+// slots each: 221 KB of shared memory at d = 128 with 12 warps.
+template <int NT>
 struct DecodeShape {
-  static constexpr int kWarps = NT == 1 ? 11 : 7;
-  static constexpr int kSlots = 48 / GR;
-  static constexpr int kCompute = 32 * kWarps;  // compute threads
-  static constexpr int kThreads = kCompute + 32;
-  static constexpr int kFetch = 8;  // pages issued together
-  static_assert(kSlots > kWarps + kFetch && 32 % kFetch == 0, "see the copying warp");
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
 };
+constexpr int kDecMaxWarps = 12;
 
 // The weights carry 2^kShift: V steps s from 2^-40 (below, the products with
 // codes of 2^-133 lose bits) to 2^60 (above, sums over long rows overflow).
 constexpr float kShift = 48.f;
-constexpr int kDecMinPages = 8;  // per CTA, where the list is short
+constexpr int kDecMinPages = 12;  // per CTA, where the list is short
 
-// Workspace: status and tickets (zeroed by the call), then parts, the rows'
-// log2-sum-exp and the scores (the last two only where weights are asked for).
+// Workspace: status and tickets (zeroed by the call), then two parts a CTA and
+// two a warp, the rows' log2-sum-exp and the scores (the last two only where
+// weights are asked for).
 struct DecodeLayout {
   int HT = 0;       // query heads a row: 4, 8 or 16
   int HC = 1;       // rows per KV head
@@ -79,7 +75,8 @@ struct DecodeLayout {
     L.part_floats = (size_t)L.HT * (d + 2);
     L.off_tick = kStatusBytes;
     L.off_part = align_up(L.off_tick + sizeof(int) * (size_t)B * Hkv * L.HC, 256);
-    L.off_lse = align_up(L.off_part + sizeof(float) * 2 * (size_t)sms * L.part_floats, 256);
+    L.off_lse = align_up(
+        L.off_part + sizeof(float) * 2 * (size_t)sms * (1 + kDecMaxWarps) * L.part_floats, 256);
     L.off_score = L.off_lse;
     L.total = L.off_lse;
     if (weights) {
@@ -101,7 +98,8 @@ struct DecodeParams {
   float* lse;
   int* status;
   int* ticket;
-  float* parts;
+  float* parts;       // [gridDim][2] of the CTAs
+  float* warp_parts;  // [gridDim][warps][2]
   float* lse2;   // [B][Hq] log2-sum-exp, or null
   float* score;  // [B][Hkv][slots][Gp] scores times scale, or null
   int64_t slots;
@@ -128,28 +126,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
-}
-
-// Waits until *count > i, with the limits of mbar_wait.
-__device__ __forceinline__ bool wait_count(const int* count, int i, const WaitCtx& w) {
-  auto now = [&]() {
-    int x;
-    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(x) : "r"(smem_u32(count)) : "memory");
-    return x;
-  };
-  if (now() > i) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (now() > i) return true;
-    if ((it & 255u) == 0) {
-      if (*w.abort_cta) return false;
-      if (globaltimer_ns() - t0 > w.limit_ns) {
-        atomicOr(w.status, VS_DEVFLAG_TIMEOUT);
-        *w.abort_cta = 1;
-        return false;
-      }
-    }
-  }
 }
 
 // D += A B, one m16n8k16 bf16 tile.
@@ -237,41 +213,82 @@ __device__ __forceinline__ void cursor_add(const DecodeParams& P, Cursor& q, int
   }
 }
 
+// What a warp needs to know of a page in one of its slots.
+struct PageNote {
+  int b, head, hc;     // the row
+  int k, pages, page;  // place in the row's list, the list's length, page (-1: not in the pool)
+};
+
+// A row that other CTAs have pages of too.
+struct SharedRow {
+  int start;      // list position of the row's first page
+  int c0, parts;  // first CTA, and how many (0: no such row)
+  int b, h0, heads, ticket;
+};
+
+__device__ __forceinline__ void write_lse(const DecodeParams& P, int b, int h, float M, float L) {
+  const float l2 = L > 0.f ? M + (log2f(L) - kShift) : (L == 0.f ? -INFINITY : L);
+  if (P.lse) P.lse[(int64_t)h * P.c.B + b] = l2 * 0.6931471805599453f;
+  if (P.lse2) P.lse2[(int64_t)b * P.Hq + h] = l2;
+}
+
+// One warp joins head h of the parts x0 .. x1 in their order: M and L in every
+// lane, four channels of the numerator in each of the first D / 4.
+template <int D, int HR, class F>
+__device__ __forceinline__ void join_parts(int x0, int x1, int h, int lane, F part_of, float& M,
+                                           float& L, float4& num) {
+  M = -INFINITY;
+  for (int x = x0 + lane; x <= x1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HR * D + h));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+  num = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = x0; p0 <= x1; p0 += 32) {
+    const int parts = min(32, x1 - p0 + 1);
+    float f = 0.f, fl = 0.f;
+    if (lane < parts) {
+      const float* p = part_of(p0 + lane) + HR * D + h;
+      f = ex2_approx(__ldcg(p) - base);
+      fl = f * __ldcg(p + HR);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) fl += __shfl_xor_sync(0xffffffffu, fl, o);
+    L += fl;
+#pragma unroll 8
+    for (int x = 0; x < parts; ++x) {
+      const float fx = __shfl_sync(0xffffffffu, f, x);
+      if (4 * lane < D)
+        axpy(num, fx, __ldcg(reinterpret_cast<const float4*>(part_of(p0 + x) + h * D + 4 * lane)));
+    }
+  }
+}
+
 // A row's query heads are the 8 NT columns of the MMAs.  PACK (up to four
 // heads): columns 0..3 and 4..7 are the same heads over two tiles of slots, as
-// two softmax states that the merge joins, so that one set of scores, weights
-// and pairs covers 32 slots.  Per 16 slots that saves some 20% of the
-// instructions, which is what bounds the loop: 4 x 128K slots at 4 query heads
-// a KV head and d = 128 take 125 us packed and 131 us not.
+// two softmax states that are joined at the row's end, so that one set of
+// scores, weights and pairs covers 32 slots.  Per 16 slots that saves some 20%
+// of the instructions, which is what bounds the loop.
 template <int GR, int NT, bool PACK>
-__global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
+__global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
     kv4_decode_kernel(const DecodeParams P) {
   static_assert(!PACK || NT == 1, "packing is for few heads");
   constexpr int D = 64 * GR, HT = 8 * NT;
   constexpr int HR = PACK ? 4 : HT;  // query heads a row
   constexpr int kSub = HT / HR;      // softmax states of a head in a warp
-  using Shape = DecodeShape<GR, NT>;
-  constexpr int kDecWarps = Shape::kWarps, kSlots = Shape::kSlots, kDecThreads = Shape::kCompute;
-  constexpr int kFetch = Shape::kFetch;
-  // floats of a warp's part of a row (O [HT][D], m and l [HT]) and of a CTA's
-  constexpr int kWarpPart = HT * (D + 2), kPart = HR * (D + 2);
+  constexpr int kWarps = DecodeShape<NT>::kWarps, kThreads = DecodeShape<NT>::kThreads;
+  constexpr int kPart = HR * (D + 2);  // floats of a part: O [HR][D], m and l [HR]
   constexpr int kChunk = GR * kKv4GroupBytes;
   // tiles of 16 slots a step (their chains of dependent instructions overlap),
   // and sets of scores
   constexpr int TT = PACK ? 4 : 2, U = TT / kSub;
-  extern __shared__ __align__(128) uint8_t smem[];
-  // ring [slot][kChunk]; the slot of a warp's last page of a row also carries
-  // its part to the merge
-  static_assert(sizeof(float) * kWarpPart <= kChunk, "a part fits a slot");
-  __shared__ __align__(8) uint64_t bars[2 * kSlots];  // full, empty
-  __shared__ bool s_valid[kSlots];                    // a page of the pool
-  __shared__ int s_abort, s_last, s_issued;  // s_issued: pages copied or on their way
-  __shared__ int s_sum[kDecWarps + 1], s_long[kDecWarps + 1];
+  extern __shared__ __align__(128) uint8_t smem[];  // [warp][2][kChunk]
+  __shared__ __align__(8) uint64_t bars[2 * kWarps];
+  __shared__ PageNote s_note[2 * kWarps];
+  __shared__ int s_abort, s_last[2];
+  __shared__ int s_sum[kWarps], s_long[kWarps];
   __shared__ int s_start[2];
-  __shared__ const float* s_part[kDecWarps];
-  static_assert(kDecWarps * kSub <= 32, "a lane each in the merge");
-  __shared__ float s_fac[32][HR], s_join[2 * HR], s_inv[HR];
-  constexpr int kJoin = (HR * D + 4 * kDecThreads - 1) / (4 * kDecThreads);
+  __shared__ SharedRow s_row[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const Kv4Cache& c = P.c;
@@ -279,14 +296,13 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
 
   if (tid == 0) {
     s_abort = 0;
-    s_issued = 0;
-    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    s_row[0].parts = s_row[1].parts = 0;
+    for (int i = 0; i < 2 * kWarps; ++i) mbar_init(smem_u32(&bars[i]), 1);
     fence_mbar_init();
   }
   // the list's length, and where this CTA's range starts: thread i sums a
   // contiguous piece of the sequences
-  constexpr int kAll = Shape::kThreads;
-  const int per = (c.B + kAll - 1) / kAll;
+  const int per = (c.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
   int mine = 0, longest = 0;
   for (int b = b0; b < b1; ++b) {
@@ -311,14 +327,14 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
   __syncthreads();
   int total = 0, before = incl - mine;
 #pragma unroll
-  for (int w = 0; w <= kDecWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
     longest = max(longest, s_long[w]);
   }
   // Rows of no more pages than there are warps, and no more rows than CTAs: a
-  // row each, so that nothing is shared.  Else equal ranges of the list.
-  const bool by_row = longest <= kDecWarps && c.B * RPS <= (int)gridDim.x;
+  // row each, so that no CTAs share one.  Else equal ranges of the list.
+  const bool by_row = longest <= kWarps && c.B * RPS <= (int)gridDim.x;
   const int share = max(kDecMinPages, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   int f0 = min((int64_t)blockIdx.x * share, (int64_t)total);
   int f1 = min((int64_t)f0 + share, (int64_t)total);
@@ -354,555 +370,499 @@ __global__ void __launch_bounds__(DecodeShape<GR, NT>::kThreads, 1)
     int n;
     kv4_len(c, b, n);
     if (n > 0) continue;
-    for (int e = tid; e < P.Hq * D; e += kAll)
+    for (int e = tid; e < P.Hq * D; e += kThreads)
       P.O[(int64_t)b * P.q_stride + e] = __float2bfloat16_rn(0.f);
     if (P.lse)
-      for (int h = tid; h < P.Hq; h += kAll) P.lse[(int64_t)h * c.B + b] = -INFINITY;
+      for (int h = tid; h < P.Hq; h += kThreads) P.lse[(int64_t)h * c.B + b] = -INFINITY;
   }
   __syncthreads();
   if (f0 >= f1) return;
 
-  Cursor seg;  // the CTA's walk, row by row
+  Cursor seg;  // where the CTA's range starts
   seg.b = s_start[0];
   cursor_load(P, seg);
   seg.k = s_start[1] % seg.v.pages;
   seg.head = s_start[1] / seg.v.pages / P.HC;
   seg.hc = s_start[1] / seg.v.pages % P.HC;
   const int count = f1 - f0;
+  const int wper = (count + kWarps - 1) / kWarps;  // pages a warp
   const WaitCtx wc{P.wait_limit_ns, P.status, &s_abort};
-  // Page i of the CTA's range goes to slot i mod kSlots and compute warp i mod kDecWarps.
-  auto full = [&](int slot) { return smem_u32(&bars[slot]); };
-  auto empty = [&](int slot) { return smem_u32(&bars[kSlots + slot]); };
 
-  if (warp == kDecWarps) {
-    // ------------------------------------------------------- copies
-    // Lane q looks up the pages q, q + 32, ...; the whole warp waits for the
-    // slots of kFetch pages, one after the other, and their lanes issue.  A
-    // slot that a merge holds back is among its row's last kDecWarps pages; all
-    // pages of that row are issued by then, for the ring has more slots than
-    // kDecWarps + kFetch.
-    auto source = [&]() {
-      return kv4_page(c, seg.b, seg.k < seg.v.first ? seg.k : seg.k + seg.v.gap, seg.head);
-    };
+  // ------------------------------------------------- this warp's own pages
+  {
+    const int w0 = min(warp * wper, count), pages = min(wper, count - w0);
+    Cursor next = seg;  // of the next page to fetch
+    int issued = 0;
     const uint8_t* src = nullptr;
-    if (lane < count) {
-      cursor_add(P, seg, lane);
+    auto source = [&]() {
+      return kv4_page(c, next.b, next.k < next.v.first ? next.k : next.k + next.v.gap, next.head);
+    };
+    if (pages > 0) {
+      cursor_add(P, next, w0);
       src = source();
     }
-    int i = 0, slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int base = 0; base < count && ok; base += 32) {
-      const uint8_t* next = nullptr;  // looked up ahead of the waits
-      if (base + 32 + lane < count) {
-        cursor_add(P, seg, 32);
-        next = source();
-      }
-      for (; i < min(count, base + 32); i += kFetch) {
-        int mine = 0, at = slot;  // this lane's slot
-#pragma unroll
-        for (int q = 0; q < kFetch; ++q) {
-          if (i + q >= kSlots && i + q < count)
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(empty(at), phase ^ 1u, wc));
-          if (lane == i - base + q) mine = at;
-          if (++at == kSlots) {
-            at = 0;
-            phase ^= 1u;
-          }
+    auto bar = [&](int s) { return smem_u32(&bars[2 * warp + s]); };
+    auto issue = [&]() {  // page `issued` into slot issued mod 2
+      if (issued >= pages) return;
+      const int s = issued & 1;
+      if (lane == 0) {
+        PageNote& pn = s_note[2 * warp + s];
+        pn.b = next.b;
+        pn.head = next.head;
+        pn.hc = next.hc;
+        pn.k = next.k;
+        pn.pages = next.v.pages;
+        pn.page = !src ? -1 : next.k < next.v.first ? next.k : next.k + next.v.gap;
+        if (src) {
+          mbar_arrive_expect_tx(bar(s), kChunk);
+          bulk_load(smem_u32(smem + (2 * warp + s) * kChunk), src, kChunk, bar(s));
+        } else {
+          atomicOr(P.status, VS_DEVFLAG_BOUNDS);
+          mbar_arrive(bar(s));
         }
-        slot = at;
-        if (!ok) break;
-        if (lane >= i - base && lane < i - base + kFetch && base + lane < count) {
-          s_valid[mine] = src != nullptr;
-          if (src) {
-            mbar_arrive_expect_tx(full(mine), kChunk);
-            bulk_load(smem_u32(smem + mine * kChunk), src, kChunk, full(mine));
-          } else {
-            atomicOr(P.status, VS_DEVFLAG_BOUNDS);
-            mbar_arrive(full(mine));
-          }
-        }
-        __syncwarp();
-        if (lane == 0)
-          asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&s_issued)),
-                       "r"(i + kFetch)
-                       : "memory");
       }
-      src = next;
-    }
-    // every copy lands before shared memory is released: the ring's last turn
-    // (the earlier ones have been used up)
-    i = min(i, count);
-    for (int x = max(0, i - kSlots); x < i; ++x)
-      mbar_wait_drain(full(x % kSlots), (uint32_t)(x / kSlots) & 1u, P.wait_limit_ns);
-    return;
-  }
+      if (++issued < pages) {
+        cursor_add(P, next, 1);
+        src = source();  // used only when its slot is free
+      }
+    };
+    issue();
+    issue();
 
-  int slot = warp;  // of this warp's next page
-  uint32_t phase = 0;
-  auto compute_sync = [&]() {  // the compute warps, each converged
-    __syncwarp();
-    named_bar_sync(1, kDecThreads);
-  };
-  bool ok = true;
-  for (int at = 0; at < count;) {
-    // ---------------------------------------------- one row, pages [k0, k1)
-    const int k0 = seg.k, k1 = min(seg.v.pages, k0 + (count - at));
-    const int head = seg.head, hc = seg.hc;
-    int n;
-    kv4_len(c, seg.b, n);
-    const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
-    const int heads = min(HR, P.G - hc * HR);
-    const int h0 = head * P.G + hc * HR;  // first query head of the row
-
-    // Q as the B operand of S^T = K Q^T: head gid (mod HR), channels in the
-    // order the words' codes give, scaled by f = 2^(field - 127), odd codes' by f / 16.
-    // For this lane's heads: the groups' sums of q, in the units f 2^-133 of
-    // the scores, and what takes scores from these units to base 2.
+    int row_b = -1, row_head = 0, row_hc = 0, row_k0 = 0, row_k1 = 0, row_pages = 0;
+    bool first_row = true;
+    int n = 0, lo_slot = 0, heads = 0, h0 = 0;
     uint32_t qf[NT][GR][2][4];
     float qs[NT][GR][2], sl[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint32_t big = 0;
-#pragma unroll
-      for (int g = 0; g < GR; ++g)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint4 u = make_uint4(0, 0, 0, 0);
-          const int h = PACK ? gid & 3 : 8 * nt + gid;
-          if (h < heads)
-            u = __ldg(reinterpret_cast<const uint4*>(P.Q + (int64_t)seg.b * P.q_stride +
-                                                     (int64_t)(h0 + h) * D + 64 * g +
-                                                     8 * (2 * tig + w)));
-          qf[nt][g][w][0] = __byte_perm(u.x, u.z, 0x5410);  // channels 0, 4
-          qf[nt][g][w][1] = __byte_perm(u.x, u.z, 0x7632);  // 1, 5
-          qf[nt][g][w][2] = __byte_perm(u.y, u.w, 0x5410);
-          qf[nt][g][w][3] = __byte_perm(u.y, u.w, 0x7632);
-          // largest exponent, as the bits of |q|
-          const uint32_t x = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                      __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
-          big = max(big, max(x & 0xffffu, x >> 16));
-        }
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // max |q| f in [2^118, 2^119); f at most 2^127, and at least 2^6 (for |q|
-      // from 2^113 on), where the scale of the scores ends
-      const int field = min(254, max(133, 372 - (int)(big >> 7)));
-      const float f = pow2_field(field);
-#pragma unroll
-      for (int g = 0; g < GR; ++g) {
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = __uint_as_float(qf[nt][g][w][i] << 16) * f;
-            const float b = __uint_as_float(qf[nt][g][w][i] & 0xffff0000u) * f;
-            sum += a + b;
-            qf[nt][g][w][i] =
-                i & 1 ? pack_bf16x2(a * 0.0625f, b * 0.0625f) : pack_bf16x2(a, b);
-          }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= 0x1p-100f;
-        qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * tig) * 0x1p-33f;
-        qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4) * 0x1p-33f;
-      }
-      const float back = P.scale * pow2_field(387 - field);  // scale 2^133 / f
-      sl[nt][0] = __shfl_sync(0xffffffffu, back, 8 * tig);
-      sl[nt][1] = __shfl_sync(0xffffffffu, back, 8 * tig + 4);
-    }
     float o[NT][GR][4][4];  // O^T tiles, centred on code 8, in units of 2^-133
     float m[NT][2], nb[NT][2], l[NT][2], r[NT][GR][2];  // p = 2^(score sl + nb)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int g = 0; g < GR; ++g) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[nt][g][j][x] = 0.f;
-        r[nt][g][0] = r[nt][g][1] = 0.f;
+    bool ok = true;
+    int i = 0;
+    for (;; ++i) {
+      const int st = i & 1;
+      PageNote pn{};
+      if (i < pages) {
+        if (ok) ok = mbar_wait(bar(st), (uint32_t)(i >> 1) & 1u, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        pn = s_note[2 * warp + st];
       }
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = nb[nt][0] = nb[nt][1] = 0.f;
-    }
-    int last = -1;  // slot of this warp's last page of the row so far
-    // this warp's pages of the row
-    for (int i = at + (warp + kDecWarps - at % kDecWarps) % kDecWarps; i < at + (k1 - k0);
-         i += kDecWarps) {
-      const int k = k0 + (i - at);
-      if (last >= 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(last));
-      }
-      // The slot's previous page belongs to another warp.  Until this page has
-      // been issued, hence the previous one used up, the barrier may be a phase
-      // behind, and the parity of this page's would read as completed.
-      if (ok) ok = wait_count(&s_issued, i, wc);
-      if (ok) ok = mbar_wait(full(slot), phase, wc);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {  // a copy may still be on its way into the slot
-        last = -1;
-        continue;
-      }
-      last = slot;
-      if ((slot += kDecWarps) >= kSlots) {
-        slot -= kSlots;
-        phase ^= 1u;
-      }
-      if (!s_valid[last]) continue;
-      const uint8_t* pg = smem + last * kChunk;
-      const int page = k < seg.v.first ? k : k + seg.v.gap;
-      const int t0 = page * kKv4Page;
-      // every slot of the page visible?
-      const bool whole = t0 + kKv4Page <= n && (t0 >= lo_slot || t0 + kKv4Page <= P.sinks);
-
-      auto hidden = [&](int t) { return t >= n || (t < lo_slot && t >= P.sinks); };
-
-      // TT tiles of 16 slots a step, looped where a page has more: a short row
-      // runs the code from a cold instruction cache.
-      const int mine = PACK ? 16 * (tig >> 1) + gid : gid;  // slot of this lane's row gid
-      const int vrow = 2 * ((lane >> 2) & 3) + ((lane >> 1) & 1) + 8 * (lane & 1);
-      const int tiles = min(4, (n - t0 + 15) / 16);
-#pragma unroll 1
-      for (int tl = 0; tl < tiles; tl += TT) {
-        const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, 16 * tl + gid) + 8 * tig;
-        const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, 16 * tl + mine);
-        // rows of the byte matrices: slots in the order that makes bytes 0 and
-        // 2 of a register slots 2 tig, 2 tig + 1, and bytes 1 and 3 those + 8
-        const uint32_t vc =
-            smem_u32(pg + kv4_code_off(GR, 1, 0, 16 * tl + vrow)) + 16 * (lane >> 4);
-        float sc[U][NT][4];
-#pragma unroll
-        for (int g = 0; g < GR; ++g)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint32_t pa =
-                *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * kSub * u);
-            const uint32_t pb =
-                *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * kSub * u + 32);
-            const float sa = kv4_step(pa), sb = kv4_step(pb);
-            const float ma = kv4_min(pa), mb = kv4_min(pb);
-            float cacc[kSub][NT][4];
-#pragma unroll
-            for (int v = 0; v < kSub; ++v) {
-              const uint8_t* kt = kc + g * kKv4Codes + 512 * (kSub * u + v);
-              const uint2 wa = *reinterpret_cast<const uint2*>(kt);
-              const uint2 wb = *reinterpret_cast<const uint2*>(kt + 256);
-              const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_bf16_first(cacc[v][nt], codes_lo(wa.x), codes_lo(wb.x), codes_hi(wa.x),
-                               codes_hi(wb.x), qf[nt][g][0][0], qf[nt][g][0][1]);
-                mma_bf16(cacc[v][nt], codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb),
-                         qf[nt][g][0][2], qf[nt][g][0][3]);
-                mma_bf16(cacc[v][nt], codes_lo(wa.y), codes_lo(wb.y), codes_hi(wa.y),
-                         codes_hi(wb.y), qf[nt][g][1][0], qf[nt][g][1][1]);
-                mma_bf16(cacc[v][nt], codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb),
-                         qf[nt][g][1][2], qf[nt][g][1][3]);
-              }
-            }
-            // q.k = sum_g s (q.n) + m (q.1)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float mm = x < 2 ? ma : mb, ss = x < 2 ? sa : sb, qq = qs[nt][g][x & 1];
-                const float qn = kSub == 2 && tig >= 2 ? cacc[kSub - 1][nt][x] : cacc[0][nt][x];
-                sc[u][nt][x] = fmaf(ss, qn, g == 0 ? mm * qq : fmaf(mm, qq, sc[u][nt][x]));
-              }
-          }
-        const int ta = t0 + 16 * tl + mine;  // slot of this lane's row gid in set 0
-        if (!whole) {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (hidden(ta + 16 * kSub * u)) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
-              if (hidden(ta + 16 * kSub * u + 8)) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
-            }
-        }
-        if (P.score) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int hh = hc * HR + (PACK ? 2 * (tig & 1) : 8 * nt + 2 * tig);
-            if (hh < P.Gp) {
-              float* dst = P.score + (((int64_t)seg.b * c.Hkv + head) * P.slots + ta) * P.Gp + hh;
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                  *reinterpret_cast<float2*>(dst + (16 * kSub * u + 8 * y) * P.Gp) = make_float2(
-                      sc[u][nt][2 * y] * sl[nt][0], sc[u][nt][2 * y + 1] * sl[nt][1]);
-            }
-          }
-        }
-        // Online softmax.  The running maximum follows only when a score
-        // passes it by 2^8: the weights have room, and the lanes' maxima need
-        // not be joined for every tile.
-        bool need = false;
-        float mx[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float x = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < U; ++u) x = fmax3(x, sc[u][nt][y], sc[u][nt][y + 2]);
-            mx[nt][y] = x * sl[nt][y];
-            need |= mx[nt][y] > m[nt][y] + 8.f;
-          }
-        if (__any_sync(0xffffffffu, need)) {
+      if (i >= pages || pn.b != row_b || pn.head != row_head || pn.hc != row_hc) {
+        if (row_b >= 0) {
+          // ------------------------------------------- the row is done here
+          const bool whole_row = row_k0 == 0 && row_k1 == row_pages;
+          float* part = P.warp_parts +
+                        (size_t)(2 * (blockIdx.x * kWarps + warp) + (first_row ? 0 : 1)) * kPart;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              float x = mx[nt][y];
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              if (x > m[nt][y]) {
-                const float f = ex2_approx(m[nt][y] - x);  // 0 at first
-                m[nt][y] = x;
-                nb[nt][y] = kShift - x;
-                l[nt][y] *= f;
+              float M = m[nt][y], L = l[nt][y], f = 1.f;
 #pragma unroll
-                for (int g = 0; g < GR; ++g) {
-                  r[nt][g][y] *= f;
+              for (int s = 4; s < 32; s <<= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+              if (PACK) {  // the two halves' states
+                const float M2 = __shfl_xor_sync(0xffffffffu, M, 2);
+                const float top = fmaxf(M, M2);
+                f = ex2_approx(M - (top == -INFINITY ? 0.f : top));
+                M = top;
+                L *= f;
+                L += __shfl_xor_sync(0xffffffffu, L, 2);
+              }
+              const int h = (PACK ? 2 * (tig & 1) : 8 * nt + 2 * tig) + y;
+              const bool mine = h < heads && (!PACK || tig < 2);
+              const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays
+              if (mine && gid == 0) {
+                if (whole_row) {
+                  write_lse(P, row_b, h0 + h, M, L);
+                } else {
+                  part[HR * D + h] = M;
+                  part[HR * D + HR + h] = L;
+                }
+              }
+              __nv_bfloat16* orow =
+                  P.O + (int64_t)row_b * P.q_stride + (int64_t)(h0 + h) * D + 2 * gid;
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    o[nt][g][j][y] *= f;
-                    o[nt][g][j][y + 2] *= f;
+              for (int g = 0; g < GR; ++g) {
+                float rs = r[nt][g][y];
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // odd codes count 16 n
+                  float lo = fmaf(o[nt][g][j][y] * 0x1p100f, 0x1p33f, rs);
+                  float hi = fmaf(o[nt][g][j][y + 2] * 0x1p100f, 0x1p29f, rs);
+                  if (PACK) {
+                    lo *= f;
+                    hi *= f;
+                    lo += __shfl_xor_sync(0xffffffffu, lo, 2);
+                    hi += __shfl_xor_sync(0xffffffffu, hi, 2);
+                  }
+                  if (mine) {
+                    if (whole_row)
+                      *reinterpret_cast<uint32_t*>(orow + 64 * g + 16 * j) =
+                          pack_bf16x2(lo * inv, hi * inv);
+                    else
+                      *reinterpret_cast<float2*>(part + h * D + 64 * g + 16 * j + 2 * gid) =
+                          make_float2(lo, hi);
                   }
                 }
               }
             }
+          first_row = false;
         }
-        float p[U][NT][4];
+        if (i >= pages) break;
+        row_b = pn.b;
+        row_head = pn.head;
+        row_hc = pn.hc;
+        row_k0 = pn.k;
+        row_pages = pn.pages;
+        kv4_len(c, row_b, n);
+        lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
+        heads = min(HR, P.G - row_hc * HR);
+        h0 = row_head * P.G + row_hc * HR;  // first query head of the row
+        // Q as the B operand of S^T = K Q^T: head gid (mod HR), channels in the
+        // order the words' codes give, scaled by f = 2^(field - 127), odd codes' by f / 16.
+        // For this lane's heads: the groups' sums of q, in the units f 2^-133 of
+        // the scores, and what takes scores from these units to base 2.
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t big = 0;
+#pragma unroll
+          for (int g = 0; g < GR; ++g)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              uint4 u = make_uint4(0, 0, 0, 0);
+              const int h = PACK ? gid & 3 : 8 * nt + gid;
+              if (h < heads)
+                u = __ldg(reinterpret_cast<const uint4*>(P.Q + (int64_t)row_b * P.q_stride +
+                                                         (int64_t)(h0 + h) * D + 64 * g +
+                                                         8 * (2 * tig + w)));
+              qf[nt][g][w][0] = __byte_perm(u.x, u.z, 0x5410);  // channels 0, 4
+              qf[nt][g][w][1] = __byte_perm(u.x, u.z, 0x7632);  // 1, 5
+              qf[nt][g][w][2] = __byte_perm(u.y, u.w, 0x5410);
+              qf[nt][g][w][3] = __byte_perm(u.y, u.w, 0x7632);
+              // largest exponent, as the bits of |q|
+              const uint32_t x = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                          __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+              big = max(big, max(x & 0xffffu, x >> 16));
+            }
+          big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // max |q| f in [2^118, 2^119); f at most 2^127, and at least 2^6 (for |q|
+          // from 2^113 on), where the scale of the scores ends
+          const int field = min(254, max(133, 372 - (int)(big >> 7)));
+          const float f = pow2_field(field);
+#pragma unroll
+          for (int g = 0; g < GR; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(qf[nt][g][w][i] << 16) * f;
+                const float b = __uint_as_float(qf[nt][g][w][i] & 0xffff0000u) * f;
+                sum += a + b;
+                qf[nt][g][w][i] =
+                    i & 1 ? pack_bf16x2(a * 0.0625f, b * 0.0625f) : pack_bf16x2(a, b);
+              }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sum *= 0x1p-100f;
+            qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * tig) * 0x1p-33f;
+            qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4) * 0x1p-33f;
+          }
+          const float back = P.scale * pow2_field(387 - field);  // scale 2^133 / f
+          sl[nt][0] = __shfl_sync(0xffffffffu, back, 8 * tig);
+          sl[nt][1] = __shfl_sync(0xffffffffu, back, 8 * tig + 4);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int g = 0; g < GR; ++g) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[nt][g][j][x] = 0.f;
+            r[nt][g][0] = r[nt][g][1] = 0.f;
+          }
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = nb[nt][0] = nb[nt][1] = 0.f;
+        }
+      }
+      row_k1 = pn.k + 1;
+      if (pn.page >= 0) {
+        const uint8_t* pg = smem + (2 * warp + st) * kChunk;
+        const int t0 = pn.page * kKv4Page;
+        // every slot of the page visible?
+        const bool whole = t0 + kKv4Page <= n && (t0 >= lo_slot || t0 + kKv4Page <= P.sinks);
+        auto hidden = [&](int t) { return t >= n || (t < lo_slot && t >= P.sinks); };
+        // TT tiles of 16 slots a step, looped where a page has more: a short row
+        // runs the code from a cold instruction cache.
+        const int mine = PACK ? 16 * (tig >> 1) + gid : gid;  // slot of this lane's row gid
+        const int vrow = 2 * ((lane >> 2) & 3) + ((lane >> 1) & 1) + 8 * (lane & 1);
+        const int tiles = min(4, (n - t0 + 15) / 16);
+#pragma unroll 1
+        for (int tl = 0; tl < tiles; tl += TT) {
+          const uint8_t* kc = pg + kv4_code_off(GR, 0, 0, 16 * tl + gid) + 8 * tig;
+          const uint8_t* pr = pg + kv4_pair_off(GR, 0, 0, 16 * tl + mine);
+          // rows of the byte matrices: slots in the order that makes bytes 0 and
+          // 2 of a register slots 2 tig, 2 tig + 1, and bytes 1 and 3 those + 8
+          const uint32_t vc =
+              smem_u32(pg + kv4_code_off(GR, 1, 0, 16 * tl + vrow)) + 16 * (lane >> 4);
+          float sc[U][NT][4];
+#pragma unroll
+          for (int g = 0; g < GR; ++g)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint32_t pa =
+                  *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * kSub * u);
+              const uint32_t pb =
+                  *reinterpret_cast<const uint32_t*>(pr + g * kKv4Pairs + 64 * kSub * u + 32);
+              const float sa = kv4_step(pa), sb = kv4_step(pb);
+              const float ma = kv4_min(pa), mb = kv4_min(pb);
+              float cacc[kSub][NT][4];
+#pragma unroll
+              for (int v = 0; v < kSub; ++v) {
+                const uint8_t* kt = kc + g * kKv4Codes + 512 * (kSub * u + v);
+                const uint2 wa = *reinterpret_cast<const uint2*>(kt);
+                const uint2 wb = *reinterpret_cast<const uint2*>(kt + 256);
+                const uint32_t xa = wa.x >> 8, xb = wb.x >> 8, ya = wa.y >> 8, yb = wb.y >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma_bf16_first(cacc[v][nt], codes_lo(wa.x), codes_lo(wb.x), codes_hi(wa.x),
+                                 codes_hi(wb.x), qf[nt][g][0][0], qf[nt][g][0][1]);
+                  mma_bf16(cacc[v][nt], codes_lo(xa), codes_lo(xb), codes_hi(xa), codes_hi(xb),
+                           qf[nt][g][0][2], qf[nt][g][0][3]);
+                  mma_bf16(cacc[v][nt], codes_lo(wa.y), codes_lo(wb.y), codes_hi(wa.y),
+                           codes_hi(wb.y), qf[nt][g][1][0], qf[nt][g][1][1]);
+                  mma_bf16(cacc[v][nt], codes_lo(ya), codes_lo(yb), codes_hi(ya), codes_hi(yb),
+                           qf[nt][g][1][2], qf[nt][g][1][3]);
+                }
+              }
+              // q.k = sum_g s (q.n) + m (q.1)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float mm = x < 2 ? ma : mb, ss = x < 2 ? sa : sb, qq = qs[nt][g][x & 1];
+                  const float qn = kSub == 2 && tig >= 2 ? cacc[kSub - 1][nt][x] : cacc[0][nt][x];
+                  sc[u][nt][x] = fmaf(ss, qn, g == 0 ? mm * qq : fmaf(mm, qq, sc[u][nt][x]));
+                }
+            }
+          const int ta = t0 + 16 * tl + mine;  // slot of this lane's row gid in set 0
+          if (!whole) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (hidden(ta + 16 * kSub * u)) sc[u][nt][0] = sc[u][nt][1] = -INFINITY;
+                if (hidden(ta + 16 * kSub * u + 8)) sc[u][nt][2] = sc[u][nt][3] = -INFINITY;
+              }
+          }
+          if (P.score) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int hh = row_hc * HR + (PACK ? 2 * (tig & 1) : 8 * nt + 2 * tig);
+              if (hh < P.Gp) {
+                float* dst = P.score + (((int64_t)row_b * c.Hkv + row_head) * P.slots + ta) * P.Gp + hh;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                  for (int y = 0; y < 2; ++y)
+                    *reinterpret_cast<float2*>(dst + (16 * kSub * u + 8 * y) * P.Gp) = make_float2(
+                        sc[u][nt][2 * y] * sl[nt][0], sc[u][nt][2 * y + 1] * sl[nt][1]);
+              }
+            }
+          }
+          // Online softmax.  The running maximum follows only when a score
+          // passes it by 2^8: the weights have room, and the lanes' maxima need
+          // not be joined for every tile.
+          bool need = false;
+          float mx[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              p[u][nt][x] = ex2_approx(fmaf(sc[u][nt][x], sl[nt][x & 1], nb[nt][x & 1]));
-              l[nt][x & 1] += p[u][nt][x];
+            for (int y = 0; y < 2; ++y) {
+              float x = -INFINITY;
+#pragma unroll
+              for (int u = 0; u < U; ++u) x = fmax3(x, sc[u][nt][y], sc[u][nt][y + 2]);
+              mx[nt][y] = x * sl[nt][y];
+              need |= mx[nt][y] > m[nt][y] + 8.f;
             }
-        const uint32_t first_half = gid < 4 ? ~0u : 0u;  // columns of a pack's first tile
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int g = 0; g < GR; ++g) {
-            uint32_t pa =
-                *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * kSub * u);
-            uint32_t pb =
-                *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * kSub * u + 32);
-            if (!whole) {  // 0 * NaN of a slot never written
-              if (hidden(ta + 16 * kSub * u)) pa = 0;
-              if (hidden(ta + 16 * kSub * u + 8)) pb = 0;
-            }
-            const float sa = kv4_step(pa), sb = kv4_step(pb);
-            const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
-            uint32_t bf[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              bf[nt][0] = transpose8(pack_bf16x2(p[u][nt][0] * sa, p[u][nt][1] * sa));
-              bf[nt][1] = transpose8(pack_bf16x2(p[u][nt][2] * sb, p[u][nt][3] * sb));
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                r[nt][g][y] = fmaf(p[u][nt][y], ca, fmaf(p[u][nt][y + 2], cb, r[nt][g][y]));
-            }
-            // V^T as the A operand: a register is one tile of 16 channels, the
-            // low codes of its bytes in rows 0..7, the high ones in rows 8..15
-#pragma unroll
-            for (int v = 0; v < kSub; ++v) {
-              const uint32_t keep = v == 0 ? first_half : ~first_half;
-              uint32_t x[4];
-              load_bytes_t(x, vc + g * kKv4Codes + 512 * (kSub * u + v));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t b0 = PACK ? bf[nt][0] & keep : bf[nt][0];
-                const uint32_t b1 = PACK ? bf[nt][1] & keep : bf[nt][1];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  mma_bf16(o[nt][g][j], codes_lo(x[j]), codes_hi(x[j]), codes_lo(x[j] >> 8),
-                           codes_hi(x[j] >> 8), b0, b1);
-              }
-            }
+          if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma_bf16(o[nt][g][j], kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
+              for (int y = 0; y < 2; ++y) {
+                float x = mx[nt][y];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                if (x > m[nt][y]) {
+                  const float f = ex2_approx(m[nt][y] - x);  // 0 at first
+                  m[nt][y] = x;
+                  nb[nt][y] = kShift - x;
+                  l[nt][y] *= f;
+#pragma unroll
+                  for (int g = 0; g < GR; ++g) {
+                    r[nt][g][y] *= f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                      o[nt][g][j][y] *= f;
+                      o[nt][g][j][y + 2] *= f;
+                    }
+                  }
+                }
+              }
           }
-      }
-    }
-    // ------------------------------------------------------ merge the warps
-    // log-sum-exp of a head, and what its O is divided by (for store())
-    auto finish = [&](int h, float M, float L) {
-      s_inv[h] = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays
-      if (h >= heads) return;
-      const float l2 = L > 0.f ? M + (log2f(L) - kShift) : (L == 0.f ? -INFINITY : L);
-      if (P.lse) P.lse[(int64_t)(h0 + h) * c.B + seg.b] = l2 * 0.6931471805599453f;
-      if (P.lse2) P.lse2[(int64_t)seg.b * P.Hq + h0 + h] = l2;
-    };
-    auto store = [&](int e, const float4& num) {  // four channels of a head
-      const int h = e / D;
-      if (h >= heads) return;
-      const float inv = s_inv[h];
-      *reinterpret_cast<uint2*>(P.O + (int64_t)seg.b * P.q_stride + (int64_t)h0 * D + e) =
-          make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
-    };
-    __syncwarp();
-    float* part = nullptr;
-    if (last >= 0) {
-      part = reinterpret_cast<float*>(smem + last * kChunk);
+          float p[U][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float ls = l[nt][y];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int s = 4; s < 32; s <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
-          const int h = 8 * nt + 2 * tig + y;
-          if (gid == 0) {
-            part[HT * D + h] = m[nt][y];
-            part[HT * D + HT + h] = ls;
-          }
+              for (int x = 0; x < 4; ++x) {
+                p[u][nt][x] = ex2_approx(fmaf(sc[u][nt][x], sl[nt][x & 1], nb[nt][x & 1]));
+                l[nt][x & 1] += p[u][nt][x];
+              }
+          const uint32_t first_half = gid < 4 ? ~0u : 0u;  // columns of a pack's first tile
 #pragma unroll
-          for (int g = 0; g < GR; ++g) {
-            float rs = r[nt][g][y];
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) rs += __shfl_xor_sync(0xffffffffu, rs, s);
+            for (int g = 0; g < GR; ++g) {
+              uint32_t pa =
+                  *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * kSub * u);
+              uint32_t pb =
+                  *reinterpret_cast<const uint32_t*>(pr + (GR + g) * kKv4Pairs + 64 * kSub * u + 32);
+              if (!whole) {  // 0 * NaN of a slot never written
+                if (hidden(ta + 16 * kSub * u)) pa = 0;
+                if (hidden(ta + 16 * kSub * u + 8)) pb = 0;
+              }
+              const float sa = kv4_step(pa), sb = kv4_step(pb);
+              const float ca = fmaf(8.f, sa, kv4_min(pa)), cb = fmaf(8.f, sb, kv4_min(pb));
+              uint32_t bf[NT][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float2*>(part + h * D + 64 * g + 16 * j + 2 * gid) = make_float2(
-                  fmaf(o[nt][g][j][y] * 0x1p100f, 0x1p33f, rs),
-                  fmaf(o[nt][g][j][y + 2] * 0x1p100f, 0x1p29f, rs));  // odd codes: 16 n
-          }
-        }
-    }
-    if (lane == 0) s_part[warp] = part;
-    compute_sync();
-    const bool shared = k0 > 0 || k1 < seg.v.pages;
-    // a CTA has at most two shared rows: the one its range starts in and the
-    // one it ends in
-    float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * kPart;
-    for (int h = warp; h < HR; h += kDecWarps) {  // the factors of head h's states, a lane each
-      const float* pw = lane < kDecWarps * kSub ? s_part[lane / kSub] : nullptr;
-      const int col = h + HR * (lane % kSub);
-      const float mw = pw ? pw[HT * D + col] : -INFINITY;
-      float M = mw;
+              for (int nt = 0; nt < NT; ++nt) {
+                bf[nt][0] = transpose8(pack_bf16x2(p[u][nt][0] * sa, p[u][nt][1] * sa));
+                bf[nt][1] = transpose8(pack_bf16x2(p[u][nt][2] * sb, p[u][nt][3] * sb));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float fw = pw ? ex2_approx(mw - (M == -INFINITY ? 0.f : M)) : 0.f;
-      float L = pw ? fw * pw[HT * D + HT + col] : 0.f;
+                for (int y = 0; y < 2; ++y)
+                  r[nt][g][y] = fmaf(p[u][nt][y], ca, fmaf(p[u][nt][y + 2], cb, r[nt][g][y]));
+              }
+              // V^T as the A operand: a register is one tile of 16 channels, the
+              // low codes of its bytes in rows 0..7, the high ones in rows 8..15
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      s_fac[lane][h] = fw;
-      if (lane == 0) {
-        if (shared) {
-          out[HR * D + h] = M;
-          out[HR * D + HR + h] = L;
-        } else {
-          finish(h, M, L);
-        }
-      }
-    }
-    compute_sync();
-    for (int e = 4 * tid; e < HR * D; e += 4 * kDecThreads) {
-      const int h = e / D;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < kDecWarps; ++w)
-        if (s_part[w]) {
+              for (int v = 0; v < kSub; ++v) {
+                const uint32_t keep = v == 0 ? first_half : ~first_half;
+                uint32_t x[4];
+                load_bytes_t(x, vc + g * kKv4Codes + 512 * (kSub * u + v));
 #pragma unroll
-          for (int v = 0; v < kSub; ++v)
-            axpy(num, s_fac[w * kSub + v][h],
-                 *reinterpret_cast<const float4*>(s_part[w] + v * HR * D + e));
-        }
-      if (shared) *reinterpret_cast<float4*>(out + e) = num;
-      else store(e, num);
-    }
-    if (shared) {
-      // list positions of the row give the CTAs that share it
-      const int row0 = f0 + at - k0, row1 = row0 + seg.v.pages;
-      const int c0 = row0 / share, c1 = (row1 - 1) / share;
-      __threadfence();
-      compute_sync();
-      if (tid == 0)
-        s_last = atomicAdd(P.ticket + (seg.b * c.Hkv + seg.head) * P.HC + seg.hc, 1) == c1 - c0;
-      compute_sync();
-      if (s_last) {
-        __threadfence();
-        // CTA x's part is its first unless its range starts before the row
-        auto part_of = [&](int x) {
-          return P.parts + (size_t)(2 * x + ((int64_t)x * share < row0 ? 1 : 0)) * kPart;
-        };
-        // a warp per head: maximum over the parts, then their factors, in
-        // pieces of 32 parts, added in the parts' order
-        float4 num[kJoin];
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint32_t b0 = PACK ? bf[nt][0] & keep : bf[nt][0];
+                  const uint32_t b1 = PACK ? bf[nt][1] & keep : bf[nt][1];
 #pragma unroll
-        for (int q = 0; q < kJoin; ++q) num[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int h = warp; h < HR; h += kDecWarps) {
-          float M = -INFINITY;
-          for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HR * D + h));
+                  for (int j = 0; j < 4; ++j)
+                    mma_bf16(o[nt][g][j], codes_lo(x[j]), codes_hi(x[j]), codes_lo(x[j] >> 8),
+                             codes_hi(x[j] >> 8), b0, b1);
+                }
+              }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          if (lane == 0) {
-            s_join[HR + h] = M;
-            s_join[h] = 0.f;
-          }
-        }
-        for (int x0 = c0; x0 <= c1; x0 += 32) {
-          const int parts = min(32, c1 - x0 + 1);
-          __syncwarp();
-          for (int h = warp; h < HR; h += kDecWarps) {  // the same warp as above
-            const float M = s_join[HR + h];
-            float fx = 0.f, L = 0.f;
-            if (lane < parts) {
-              const float* px = part_of(x0 + lane) + HR * D + h;
-              fx = ex2_approx(__ldcg(px) - (M == -INFINITY ? 0.f : M));
-              L = fx * __ldcg(px + HR);
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  mma_bf16(o[nt][g][j], kMinus8, kMinus128, kMinus8, kMinus128, bf[nt][0], bf[nt][1]);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            s_fac[lane][h] = fx;
-            if (lane == 0) s_join[h] += L;
-          }
-          compute_sync();
-#pragma unroll
-          for (int q = 0; q < kJoin; ++q) {
-            const int e = 4 * (tid + q * kDecThreads);
-            if (e < HR * D) {
-#pragma unroll 4
-              for (int x = 0; x < parts; ++x)
-                axpy(num[q], s_fac[x][e / D],
-                     __ldcg(reinterpret_cast<const float4*>(part_of(x0 + x) + e)));
-            }
-          }
-          compute_sync();
-        }
-        if (tid < HR) {
-          const float M = s_join[HR + tid], L = s_join[tid];
-          finish(tid, M, L);
-        }
-        compute_sync();
-#pragma unroll
-        for (int q = 0; q < kJoin; ++q) {
-          const int e = 4 * (tid + q * kDecThreads);
-          if (e < HR * D) store(e, num[q]);
         }
       }
-    }
-    compute_sync();  // the parts in the ring are read
-    if (last >= 0) {
-      fence_proxy_async_smem();  // generic accesses of the stage before its next copy
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty(last));
+      issue();
+    }
+    // copies not awaited (only after a wait gave up) land before shared memory is released
+    if (lane == 0 && !ok)
+      for (; i < issued; ++i)
+        mbar_wait_drain(bar(i & 1), (uint32_t)(i >> 1) & 1u, P.wait_limit_ns);
+  }
+
+  // ------------------------------------- the parts of the CTA's warps, by row
+  // One (row, head) a warp and turn: a lane per part, then D / 4 lanes with
+  // four channels each.
+  __syncthreads();
+  const int w_lane = 4 * lane;  // first channel of this lane
+  auto finish = [&](int b, int h, float M, float L, const float4& num) {
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays
+    if (w_lane < D)
+      *reinterpret_cast<uint2*>(P.O + (int64_t)b * P.q_stride + (int64_t)h * D + w_lane) =
+          make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+    if (lane == 0) write_lse(P, b, h, M, L);
+  };
+  int turn = 0;
+  for (int at = 0; at < count;) {
+    const int k0 = seg.k, k1 = min(seg.v.pages, k0 + (count - at));
+    const int wa = at / wper, wb = (at + (k1 - k0) - 1) / wper;  // the warps with pages of it
+    const bool shared = k0 > 0 || k1 < seg.v.pages;
+    const int heads = min(HR, P.G - seg.hc * HR), h0 = seg.head * P.G + seg.hc * HR;
+    if (shared || wa != wb) {
+      // the CTA's part: its first row's or its last row's
+      float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * kPart;
+      for (int h = 0; h < heads; ++h, ++turn) {
+        if (turn % kWarps != warp) continue;
+        // a warp's part of the row is its first unless its range starts before the row
+        auto part_of = [&](int w) {
+          return P.warp_parts +
+                 (size_t)(2 * (blockIdx.x * kWarps + w) + (w * wper < at ? 1 : 0)) * kPart;
+        };
+        float M, L;
+        float4 num;
+        join_parts<D, HR>(wa, wb, h, lane, part_of, M, L, num);
+        if (!shared) {
+          finish(seg.b, h0 + h, M, L, num);
+        } else {
+          if (w_lane < D) *reinterpret_cast<float4*>(out + h * D + w_lane) = num;
+          if (lane == 0) {
+            out[HR * D + h] = M;
+            out[HR * D + HR + h] = L;
+          }
+        }
+      }
+      if (shared && tid == 0) {
+        // list positions of the row give the CTAs that share it
+        SharedRow& sr = s_row[at > 0 ? 1 : 0];
+        sr.start = f0 + at - k0;
+        sr.c0 = sr.start / share;
+        sr.parts = (sr.start + seg.v.pages - 1) / share - sr.c0 + 1;
+        sr.b = seg.b;
+        sr.h0 = h0;
+        sr.heads = heads;
+        sr.ticket = (seg.b * c.Hkv + seg.head) * P.HC + seg.hc;
+      }
     }
     at += k1 - k0;
     if (at < count) cursor_add(P, seg, k1 - k0);
+  }
+  // ---------------------------------------------------- rows of several CTAs
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const SharedRow& sr = s_row[tid];
+    s_last[tid] = sr.parts > 0 && atomicAdd(P.ticket + sr.ticket, 1) == sr.parts - 1;
+  }
+  __syncthreads();
+  if (!s_last[0] && !s_last[1]) return;
+  __threadfence();
+  turn = 0;
+  for (int x = 0; x < 2; ++x) {
+    if (!s_last[x]) continue;
+    const SharedRow sr = s_row[x];
+    for (int h = 0; h < sr.heads; ++h, ++turn) {
+      if (turn % kWarps != warp) continue;
+      // CTA x's part is its first unless its range starts before the row
+      auto part_of = [&](int cta) {
+        return P.parts + (size_t)(2 * cta + ((int64_t)cta * share < sr.start ? 1 : 0)) * kPart;
+      };
+      float M, L;
+      float4 num;
+      join_parts<D, HR>(sr.c0, sr.c0 + sr.parts - 1, h, lane, part_of, M, L, num);
+      finish(sr.b, sr.h0 + h, M, L, num);
+    }
   }
 }
 
@@ -940,11 +900,10 @@ size_t kv4_decode_ws_bytes(int B, int Hq, int Hkv, int d, int max_len, bool weig
 template <int GR, int NT, bool PACK>
 static cudaError_t launch_decode_impl(const DecodeParams& P, int grid, cudaStream_t stream) {
   auto kern = kv4_decode_kernel<GR, NT, PACK>;
-  constexpr int smem =
-      DecodeShape<GR, NT>::kSlots * GR * kKv4GroupBytes;
+  constexpr int smem = DecodeShape<NT>::kWarps * 2 * GR * kKv4GroupBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, DecodeShape<GR, NT>::kThreads, smem, stream>>>(P);
+  kern<<<grid, DecodeShape<NT>::kThreads, smem, stream>>>(P);
   return cudaGetLastError();
 }
 
@@ -956,6 +915,12 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
   // status word and tickets
   cudaError_t e = cudaMemsetAsync(ws, 0, L.off_part, a.stream);
   if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.c.B * a.c.Hkv * L.HC;
+  // no more CTAs than the longest possible list fills
+  const int64_t most = rows * (L.slots / kKv4Page);
+  const int64_t by_pages = (most + kDecMinPages - 1) / kDecMinPages;
+  const int64_t want = by_pages > rows ? by_pages : rows;
+  const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
   DecodeParams P;
   P.c = a.c;
   P.Q = static_cast<const __nv_bfloat16*>(a.Q);
@@ -972,16 +937,11 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
   P.status = reinterpret_cast<int*>(ws);
   P.ticket = reinterpret_cast<int*>(ws + L.off_tick);
   P.parts = reinterpret_cast<float*>(ws + L.off_part);
+  P.warp_parts = P.parts + 2 * (size_t)grid * L.part_floats;
   P.lse2 = a.acc_out ? reinterpret_cast<float*>(ws + L.off_lse) : nullptr;
   P.score = a.acc_out ? reinterpret_cast<float*>(ws + L.off_score) : nullptr;
   P.slots = L.slots;
   P.wait_limit_ns = kDefaultWaitLimitNs;
-  const int64_t rows = (int64_t)a.c.B * a.c.Hkv * L.HC;
-  // no more CTAs than the longest possible list fills
-  const int64_t most = rows * (L.slots / kKv4Page);
-  const int64_t by_pages = (most + kDecMinPages - 1) / kDecMinPages;
-  const int64_t want = by_pages > rows ? by_pages : rows;
-  const int grid = (int)(want < 1 ? 1 : (want < sms ? want : sms));
   if (L.HT == 4)
     e = a.c.GR == 1 ? launch_decode_impl<1, 1, true>(P, grid, a.stream)
                     : launch_decode_impl<2, 1, true>(P, grid, a.stream);
