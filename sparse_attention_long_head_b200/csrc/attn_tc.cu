@@ -606,19 +606,24 @@ __device__ __forceinline__ void exp_tile(const uint32_t (&sr)[4][32], float sl2,
   ls = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
-// One warp writes V rows [0, rows) of a 128-row tile, and zeros below them, in
+// One warp copies V rows [0, rows) of a 128-row tile, with zeros below them, to
 // the layout the tile's TMA load gives (64-column halves, 128-byte swizzle).
+// All copies are in flight together; they have landed on return.
 template <int D>
 __device__ __forceinline__ void load_v_tail(uint8_t* dst, const __nv_bfloat16* v, int64_t stride,
                                             int rows, int lane) {
   constexpr int CH = D / 8;  // 16-byte chunks per row
+  const uint32_t base = smem_u32(dst);
 #pragma unroll 8
   for (int e = lane; e < 128 * CH; e += 32) {
     const int r = e / CH, ch = e % CH;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(v + (int64_t)r * stride + ch * 8));
-    *reinterpret_cast<uint4*>(dst + (ch >> 3) * 16384 + sw128_off(r, ch & 7)) = x;
+    const uint32_t bytes = r < rows ? 16u : 0u;  // the rest of the 16 is zero-filled
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     base + (ch >> 3) * 16384 + sw128_off(r, ch & 7)),
+                 "l"(v + (int64_t)min(r, rows - 1) * stride + ch * 8), "r"(bytes)
+                 : "memory");
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int D, int MODE>
@@ -875,6 +880,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               mma_commit(bar(B_SFULL + sub));
             }
           mma_commit(bar(B_EMPTY + kslot));
+          // Window units are short: their Q is given back after the last S
+          // rather than at the unit's end, so that the next unit's Q arrives
+          // under the last softmax and the epilogue.
+          if (MODE == kAttnWindow && ui.n == 1) mma_commit(bar(B_QEMPTY));
           for (int k = 0; k < ui.n && ok; ++k) {
             const int fl_after = k + 2 < ui.n ? unit_item<MODE>(P, ui, k + 2).flags : 0;  // early load
             if (!mbar_wait(bar(B_STAGE + stg % S), (stg / S) & 1, wc)) { ok = false; break; }
@@ -900,6 +909,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
             }
             if (!ok) break;
+            if (MODE == kAttnWindow && k + 2 == ui.n) mma_commit(bar(B_QEMPTY));
             mma_commit(bar(B_EMPTY + vslot));
             if (k + 1 < ui.n) mma_commit(bar(B_EMPTY + kslot));
             fl = fl_next;
@@ -910,7 +920,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // empty mask row): its epilogue writes zeros from l = 0
           for (int sub = 0; sub < 2; ++sub)
             if (!started[sub]) mma_commit(bar(B_OFULL + sub));
-          mma_commit(bar(B_QEMPTY));
+          if (MODE != kAttnWindow) mma_commit(bar(B_QEMPTY));
           ++ucount;
           continue;
         }
