@@ -587,7 +587,8 @@ vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride
  *            <= keep.
  *   lens_out int32 [B], acc_out, pos_out [B][Hkv][ld_out], ld_out >=
  *            min(keep, max_len): the new lengths, and the kept slots' entries
- *            ([0, k) of each row).  Not the input buffers.
+ *            ([0, k) of each row; the rest is left as it was).  They must not
+ *            overlap the input buffers.
  * The pool is changed in place; pages that only held slots at or above k are
  * free afterwards.  The pages of a sequence that is cut must not be shared
  * with another sequence.  1 <= max_len <= 2^18.

@@ -176,8 +176,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()  # an int: the declared argtypes make it a pointer
 
 
+# The current stream's handle without a Stream object (3 us of every call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -286,6 +294,8 @@ def vs_window_attn_fwd(Q, K, V, window, sinks, O, lse, ws, softmax_scale=0.0, st
     None; ws of 256 bytes."""
     N, Hq, d = Q.shape
     Hkv = K.shape[1]
+    for t, like in ((Q, None), (O, Q), (K, None), (V, K)):
+        _rows(t, like)
     _check(lib().vs_window_attn_fwd(_ptr(Q), _ptr(K), _ptr(V), _dtype(Q), N, Hq, Hkv, d,
                                     Q.stride(0), K.stride(0), float(softmax_scale), int(window),
                                     int(sinks), _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
@@ -297,6 +307,8 @@ def vs_window_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, window, sinks, O,
     T, Hq, d = Q.shape
     Hkv = K.shape[1]
     B = cu_seqlens.numel() - 1
+    for t, like in ((Q, None), (O, Q), (K, None), (V, K)):
+        _rows(t, like)
     _check(lib().vs_window_attn_fwd_varlen(
         _ptr(Q), _ptr(K), _ptr(V), _dtype(Q), T, B, _ptr(cu_seqlens), int(max_seqlen), Hq, Hkv, d,
         Q.stride(0), K.stride(0), float(softmax_scale), int(window), int(sinks), _ptr(O),
@@ -463,6 +475,14 @@ def vs_kv4_evict_workspace_size(B: int, Hkv: int, max_len: int, keep: int) -> in
     return int(lib().vs_kv4_evict_workspace_size(B, Hkv, max_len, keep))
 
 
+def _rows(t, like=None):
+    """Checks [tokens, heads, d] with packed heads (and the row stride of `like`)."""
+    _, H, d = t.shape
+    st = t.stride()
+    assert st[2] == 1 and (H == 1 or st[1] == d), "heads of a row must be contiguous"
+    assert like is None or (t.dtype == like.dtype and st[0] == like.stride(0)), "rows must match"
+
+
 _KV4_HEAD_DIM = {4608: 64, 9216: 128}  # bytes per page and head -> d
 
 
@@ -476,9 +496,10 @@ def _kv4_dims(pool):
     return n_pages, Hkv, d
 
 
-def _kv4_max(table, max_len=None):
+def _kv4_max(table, lens, max_len=None):
     """The bound on lengths that a page table [B, pages] gives, checked against the caller's."""
-    assert table.dtype == torch.int32 and table.stride(1) == 1
+    assert table.dtype == lens.dtype == torch.int32 and table.stride(1) == 1
+    assert table.shape[0] >= lens.numel() and lens.is_contiguous()
     room = min(64 * table.shape[1], 1 << 24)
     if max_len is None:
         return room
@@ -503,7 +524,9 @@ def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=Non
     [B, pages]; lens int32 [B], the new tokens included; acc fp32 and pos int32 [B, Hkv, ld]."""
     T = K.shape[0]
     n_pages, Hkv, d = _kv4_dims(pool)
-    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and V.stride(0) == K.stride(0)
+    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape
+    _rows(K)
+    _rows(V, K)
     B = cu_seqlens.numel() - 1
     rows = acc if acc is not None else pos
     ld = 0 if rows is None else _kv4_rows(rows)
@@ -512,7 +535,7 @@ def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=Non
     assert A_v is None or (A_v.shape[1] == T and A_v.is_contiguous())
     _check(lib().vs_kv4_append(_ptr(K), _ptr(V), _dtype(K), T, _ptr(cu_seqlens), int(max_new),
                                K.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
-                               _ptr(lens), _ptr(n_tokens), B, _kv4_max(table), Hq, Hkv, d,
+                               _ptr(lens), _ptr(n_tokens), B, _kv4_max(table, lens), Hq, Hkv, d,
                                _ptr(A_v), _ptr(acc), _ptr(pos), ld, _ptr(ws), ws.numel(),
                                _stream(stream)), "vs_kv4_append")
 
@@ -521,10 +544,11 @@ def vs_kv4_read(pool, table, lens, start, cu_seqlens, max_read, K, V, ws, stream
     """Slots [start[b], start[b] + n_b) into rows [cu[b], cu[b + 1]) of K, V [T, Hkv, d] bf16;
     start int32 [B] or None."""
     n_pages, Hkv, d = _kv4_dims(pool)
-    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and V.stride(0) == K.stride(0)
-    assert K.dtype == V.dtype == torch.bfloat16
+    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and K.dtype == torch.bfloat16
+    _rows(K)
+    _rows(V, K)
     _check(lib().vs_kv4_read(_ptr(pool), n_pages, _ptr(table), table.stride(0), _ptr(lens),
-                             _ptr(start), cu_seqlens.numel() - 1, _kv4_max(table), Hkv, d,
+                             _ptr(start), cu_seqlens.numel() - 1, _kv4_max(table, lens), Hkv, d,
                              _ptr(cu_seqlens), int(max_read), K.shape[0], _ptr(K), _ptr(V),
                              K.stride(0), _ptr(ws), ws.numel(), _stream(stream)), "vs_kv4_read")
 
@@ -534,12 +558,14 @@ def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, 
     """Q, O [B, Hq, d] bf16; lse fp32 [Hq, B] or None; acc_in, acc_out fp32 [B, Hkv, ld] or None."""
     B, Hq, d = Q.shape
     n_pages, Hkv, dp = _kv4_dims(pool)
-    assert dp == d and O.shape == Q.shape and O.stride(0) == Q.stride(0)
+    assert dp == d and O.shape == Q.shape
+    _rows(Q)
+    _rows(O, Q)
     ld = 0 if acc_out is None else _kv4_rows(acc_out)
     assert acc_in is None or acc_out is None or _kv4_rows(acc_in) == ld
     _check(lib().vs_kv4_decode_attn_fwd(
         _ptr(Q), _dtype(Q), Q.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
-        _ptr(lens), B, _kv4_max(table, max_len), Hq, Hkv, d, float(softmax_scale), int(window),
+        _ptr(lens), B, _kv4_max(table, lens, max_len), Hq, Hkv, d, float(softmax_scale), int(window),
         int(sinks), _ptr(acc_in), _ptr(acc_out), ld, _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
         _stream(stream)), "vs_kv4_decode_attn_fwd")
 
@@ -552,7 +578,7 @@ def vs_kv4_evict(pool, table, lens, n_tokens, max_len, acc, pos, keep, sinks, re
     ld, ld_out = _kv4_rows(acc), _kv4_rows(acc_out)
     assert _kv4_rows(pos) == ld and _kv4_rows(pos_out) == ld_out
     _check(lib().vs_kv4_evict(_ptr(pool), n_pages, _ptr(table), table.stride(0), _ptr(lens),
-                              _ptr(n_tokens), B, _kv4_max(table, max_len), Hkv, d, _ptr(acc), _ptr(pos), ld,
+                              _ptr(n_tokens), B, _kv4_max(table, lens, max_len), Hkv, d, _ptr(acc), _ptr(pos), ld,
                               int(keep), int(sinks), int(recent), _ptr(lens_out), _ptr(acc_out),
                               _ptr(pos_out), ld_out, _ptr(ws), ws.numel(), _stream(stream)),
            "vs_kv4_evict")

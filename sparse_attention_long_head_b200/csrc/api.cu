@@ -101,7 +101,7 @@ const char* vs_status_string(vs_status s) {
   return "VS_ERR_UNKNOWN";
 }
 
-int vs_version(void) { return 100; }
+int vs_version(void) { return 200; }
 
 vs_status vs_index_scores(const void* K, const void* V, vs_dtype dtype, int N, int Hkv, int d,
                           int64_t stride_tok, int64_t stride_head, const float* W1,

@@ -135,7 +135,10 @@ def test_page_bytes_and_binding_checks():
     assert pool.shape == (3, 2, 4608)
     q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):  # more slots than the table's four pages hold
-        vs.vs_kv4_decode_attn_fwd(q, pool, table, table[:, 0], 257, q, None, vs.workspace(256, "cpu"))
+        vs.vs_kv4_decode_attn_fwd(q, pool, table, table[:, 0].contiguous(), 257, q, None, vs.workspace(256, "cpu"))
+    with pytest.raises(AssertionError):  # heads with a gap between them
+        vs.vs_kv4_decode_attn_fwd(torch.zeros((2, 8, 64), dtype=torch.bfloat16)[:, ::2], pool, table, table[:, 0].contiguous(),
+                                  256, q, None, vs.workspace(256, "cpu"))
     with pytest.raises(ValueError):
-        vs.vs_kv4_decode_attn_fwd(q, torch.zeros((3, 2, 100), dtype=torch.uint8), table, table[:, 0], 256, q, None,
+        vs.vs_kv4_decode_attn_fwd(q, torch.zeros((3, 2, 100), dtype=torch.uint8), table, table[:, 0].contiguous(), 256, q, None,
                                   vs.workspace(256, "cpu"))
