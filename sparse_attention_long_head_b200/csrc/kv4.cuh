@@ -61,6 +61,30 @@ __device__ __forceinline__ float kv4_min(uint32_t pair) {
   return __uint_as_float(pair & 0xffff0000u);
 }
 
+// A second kernel that starts while the first drains (programmatic dependent
+// launch): the first calls launch_dependents, the second waits for all of the
+// first's writes before it touches anything.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                                A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 struct Kv4AppendArgs {
   Kv4Cache c;
   const void* K;

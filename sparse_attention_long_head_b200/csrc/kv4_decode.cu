@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
   const Kv4Cache& c = P.c;
   const int RPS = c.Hkv * P.HC;  // rows per sequence
 
+  launch_dependents();
   if (tid == 0) {
     s_abort = 0;
     s_row[0].parts = s_row[1].parts = 0;
@@ -867,29 +868,37 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
 }
 
 // acc_out = acc_in + sum over the KV head's query heads of the softmax weight,
-// per slot; invisible slots keep their sum.
+// per slot; invisible slots keep their sum.  Bound by memory: a float per query
+// head and two for acc per slot.  W: floats of a score load (Gp is a multiple).
+template <int W>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const float* acc_in,
                                                           float* acc_out, int64_t ld) {
+  wait_for_previous_kernel();
   const Kv4Cache& c = P.c;
   const int b = blockIdx.y / c.Hkv, head = blockIdx.y % c.Hkv;
   int n;
   kv4_len(c, b, n);
   const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
   const float* lse2 = P.lse2 + (int64_t)b * P.Hq + (int64_t)head * P.G;
+  const int64_t row = (int64_t)b * c.Hkv + head;
   for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
-    const int64_t at = ((int64_t)b * c.Hkv + head) * ld + t;
-    float sum = acc_in ? acc_in[at] : 0.f;
+    float sum = acc_in ? acc_in[row * ld + t] : 0.f;
     if ((t >= lo_slot || t < P.sinks) && kv4_page(c, b, t >> 6, head)) {
-      const float* s = P.score + (((int64_t)b * c.Hkv + head) * P.slots + t) * P.Gp;
+      const float* s = P.score + (row * P.slots + t) * P.Gp;
       float w = 0.f;
-      for (int h = 0; h < P.G; h += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(s + h);
-        w += ex2_approx(x.x - __ldg(lse2 + h));
-        if (h + 1 < P.G) w += ex2_approx(x.y - __ldg(lse2 + h + 1));
+      for (int h = 0; h < P.G; h += W) {
+        float x[W];
+        if constexpr (W == 4)
+          *reinterpret_cast<float4*>(x) = __ldcs(reinterpret_cast<const float4*>(s + h));
+        else
+          *reinterpret_cast<float2*>(x) = __ldcs(reinterpret_cast<const float2*>(s + h));
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (h + i < P.G) w += ex2_approx(x[i] - __ldg(lse2 + h + i));
       }
       sum += w;
     }
-    acc_out[at] = sum;
+    acc_out[row * ld + t] = sum;
   }
 }
 
@@ -953,11 +962,10 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
                     : launch_decode_impl<2, 2, false>(P, grid, a.stream);
   if (e != cudaSuccess || !a.acc_out) return e;
   const int64_t per_row = (L.slots + 255) / 256;
-  const int64_t cap = ceil_div(16LL * sms, a.c.B * a.c.Hkv);
-  const int gx = (int)(per_row < cap ? per_row : cap);
-  kv4_weights_kernel<<<dim3(gx < 1 ? 1 : gx, a.c.B * a.c.Hkv), 256, 0, a.stream>>>(P, a.acc_in,
-                                                                                  a.acc_out, a.ld);
-  return cudaGetLastError();
+  const int64_t cap = ceil_div(32LL * sms, a.c.B * a.c.Hkv);
+  const dim3 wgrid((unsigned)(per_row < cap ? per_row : cap), a.c.B * a.c.Hkv);
+  return launch_after(L.Gp % 4 == 0 ? kv4_weights_kernel<4> : kv4_weights_kernel<2>, wgrid, 256,
+                      a.stream, P, a.acc_in, a.acc_out, a.ld);
 }
 
 }  // namespace vs

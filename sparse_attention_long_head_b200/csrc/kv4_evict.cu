@@ -42,10 +42,17 @@ struct EvictShared {
   uint32_t total_a, total_b;  // read by the cluster
 };
 
+// Where a histogram keeps digit d: lane l of a warp reads digits 255 - 8 l - i,
+// i = 0..7, without bank conflicts.
+__device__ __forceinline__ uint32_t bin_at(uint32_t d) {
+  return 32 * ((255 - d) & 7) + ((255 - d) >> 3);
+}
+
 // kEvThreads threads of V slots each.
 template <int kEvThreads, int V>
 __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
     kv4_evict_kernel(Kv4EvictArgs a, int32_t* counts, int32_t* lists, int64_t list_ld) {
+  launch_dependents();  // every CTA is resident or done by the time the moves start
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   auto sync_all = [&]() {
@@ -124,21 +131,32 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+      if (w0 + 32 * j >= w1) break;  // uniform over the warp
       if (live(j) && (pass == 0 || (key[j] >> (shift + 8)) == prefix))
-        atomicAdd(&sh.hist[pass][(key[j] >> shift) & 255u], 1u);
-    sync_all();
-    if (tid < 256) {
-      uint32_t x = 0;
-      for (int r = 0; r < C; ++r) x += cl.map_shared_rank(sh.hist[pass], r)[tid];
-      sh.merged[32 * ((255 - tid) & 7) + ((255 - tid) >> 3)] = x;  // as it is read below
+        atomicAdd(&sh.hist[pass][bin_at((key[j] >> shift) & 255u)], 1u);
     }
-    __syncthreads();
+    sync_all();
+    const uint32_t* merged = sh.hist[pass];
+    if (C > 1) {
+      if (tid < 256) {
+        uint32_t x[kEvMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kEvMaxCluster; ++r)  // all reads in flight
+          x[r] = r < C ? cl.map_shared_rank(sh.hist[pass], r)[tid] : 0u;
+        uint32_t sum = 0;
+#pragma unroll
+        for (int r = 0; r < kEvMaxCluster; ++r) sum += x[r];
+        sh.merged[tid] = sum;
+      }
+      __syncthreads();
+      merged = sh.merged;
+    }
     // every warp takes the same decision: lane l holds bins 255 - 8 l downwards
     uint32_t part[8], mine = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      part[i] = sh.merged[32 * i + lane];  // bin 255 - (8 lane + i)
+      part[i] = merged[32 * i + lane];  // bin 255 - (8 lane + i)
       mine += part[i];
     }
     uint32_t incl = mine;
@@ -203,7 +221,10 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
   if (equal != need) {       // uniform over the cluster
     uint32_t eq = 0, none;
 #pragma unroll
-    for (int j = 0; j < V; ++j) eq += __popc(__ballot_sync(0xffffffffu, live(j) && key[j] == bound));
+    for (int j = 0; j < V; ++j) {
+      if (w0 + 32 * j >= w1) break;
+      eq += __popc(__ballot_sync(0xffffffffu, live(j) && key[j] == bound));
+    }
     exchange(eq, 0, ties_before, none);
   }
   // who stays: bit j of `stay` for key j
@@ -211,6 +232,7 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
   uint32_t holes = 0, movers = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
+    if (w0 + 32 * j >= w1) break;
     const int t = w0 + 32 * j + lane;
     const bool tie = t < w1 && key[j] == bound;
     bool s = t < w1 && (key[j] > bound || tie);
@@ -230,6 +252,7 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
   int32_t* mover_list = hole_list + list_ld;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
+    if (w0 + 32 * j >= w1) break;
     const int t = w0 + 32 * j + lane;
     const bool s = (stay >> j) & 1u;
     const bool hole = t < w1 && t < k && !s, mover = t >= k && s;
@@ -271,6 +294,7 @@ constexpr int kMoves = 4;
 
 __global__ void __launch_bounds__(kMoveThreads)
     kv4_move_kernel(Kv4EvictArgs a, const int32_t* counts, const int32_t* lists, int64_t list_ld) {
+  wait_for_previous_kernel();
   const Kv4Cache& c = a.c;
   const int row = blockIdx.y, b = row / c.Hkv, head = row % c.Hkv;
   const int moves = counts[row];
@@ -375,9 +399,10 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
   int32_t* lists = counts + rows;
   const int64_t list = evict_moves(a.c.max_len, a.keep);
   // Rows of up to 8192 slots take one CTA of 512 threads (two fit an SM, and no
-  // cluster barrier is needed).  Longer rows take clusters of 1024 threads:
-  // as many CTAs as the slots need at 16 a thread, more while the device has
-  // SMs to spare; from 131072 slots on, 32 a thread.
+  // cluster barrier is needed).  Longer rows take clusters: as many CTAs as the
+  // slots need, more while the device has SMs to spare, of 512 threads (at most
+  // 15 clusters of 8 CTAs of 1024 threads fit the device: 16 rows of 131072
+  // slots took two turns, 70 against 67 us), above 131072 slots of 1024.
   const int n = a.c.max_len;
   int C = 1;
   if (n > 8192)
@@ -385,14 +410,13 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
   if (n <= 2048) e = launch_evict_impl<512, 4>(a, C, counts, lists, list);
   else if (n <= 8192) e = launch_evict_impl<512, 16>(a, C, counts, lists, list);
   else if (C * 4096 >= n) e = launch_evict_impl<1024, 4>(a, C, counts, lists, list);
-  else if (C * 16384 >= n) e = launch_evict_impl<1024, 16>(a, C, counts, lists, list);
+  else if (C * 16384 >= n) e = launch_evict_impl<512, 32>(a, C, counts, lists, list);
   else e = launch_evict_impl<1024, 32>(a, C, counts, lists, list);
   if (e != cudaSuccess || list == 0) return e;
   const int64_t per_block = (kMoveThreads / 16) * kMoves;
   const int64_t want = (list + per_block - 1) / per_block, cap = ceil_div(16LL * sms, rows);
-  kv4_move_kernel<<<dim3((unsigned)(want < cap ? want : cap), rows), kMoveThreads, 0, a.stream>>>(
-      a, counts, lists, list);
-  return cudaGetLastError();
+  return launch_after(kv4_move_kernel, dim3((unsigned)(want < cap ? want : cap), rows),
+                      kMoveThreads, a.stream, a, (const int*)counts, (const int*)lists, list);
 }
 
 }  // namespace vs
