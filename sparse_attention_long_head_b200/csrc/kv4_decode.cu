@@ -237,6 +237,35 @@ __device__ __forceinline__ void write_lse(const DecodeParams& P, int b, int h, f
 template <int D, int HR, class F>
 __device__ __forceinline__ void join_parts(int x0, int x1, int h, int lane, F part_of, float& M,
                                            float& L, float4& num) {
+  constexpr int kFew = 4;
+  if (x1 - x0 < kFew) {  // few parts (short rows): one trip to memory for everything
+    float m = -INFINITY, l = 0.f;
+    if (lane <= x1 - x0) {
+      m = __ldcg(part_of(x0 + lane) + HR * D + h);
+      l = __ldcg(part_of(x0 + lane) + HR * D + HR + h);
+    }
+    float4 y[kFew];
+#pragma unroll
+    for (int x = 0; x < kFew; ++x)
+      if (x <= x1 - x0 && 4 * lane < D)
+        y[x] = __ldcg(reinterpret_cast<const float4*>(part_of(x0 + x) + h * D + 4 * lane));
+    M = m;
+#pragma unroll
+    for (int o = kFew / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = __shfl_sync(0xffffffffu, M, 0);
+    const float f = ex2_approx(m - (M == -INFINITY ? 0.f : M));
+    L = 0.f;
+    num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kFew; ++x) {
+      const float fx = __shfl_sync(0xffffffffu, f, x), lx = __shfl_sync(0xffffffffu, l, x);
+      if (x <= x1 - x0) {
+        L = fmaf(fx, lx, L);
+        if (4 * lane < D) axpy(num, fx, y[x]);
+      }
+    }
+    return;
+  }
   M = -INFINITY;
   for (int x = x0 + lane; x <= x1; x += 32) M = fmaxf(M, __ldcg(part_of(x) + HR * D + h));
 #pragma unroll
@@ -394,13 +423,12 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
     const int w0 = min(warp * wper, count), pages = min(wper, count - w0);
     Cursor next = seg;  // of the next page to fetch
     int issued = 0;
-    const uint8_t* src = nullptr;
-    auto source = [&]() {
-      return kv4_page(c, next.b, next.k < next.v.first ? next.k : next.k + next.v.gap, next.head);
-    };
+    int id = 0;  // of the next page, looked up one page ahead of its use
+    auto next_page = [&]() { return next.k < next.v.first ? next.k : next.k + next.v.gap; };
+    auto look_up = [&]() { id = __ldg(c.table + (int64_t)next.b * c.table_ld + next_page()); };
     if (pages > 0) {
       cursor_add(P, next, w0);
-      src = source();
+      look_up();
     }
     auto bar = [&](int s) { return smem_u32(&bars[2 * warp + s]); };
     auto issue = [&]() {  // page `issued` into slot issued mod 2
@@ -413,10 +441,12 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
         pn.hc = next.hc;
         pn.k = next.k;
         pn.pages = next.v.pages;
-        pn.page = !src ? -1 : next.k < next.v.first ? next.k : next.k + next.v.gap;
-        if (src) {
+        const bool valid = id >= 0 && id < c.n_pages;
+        pn.page = valid ? next_page() : -1;
+        if (valid) {
           mbar_arrive_expect_tx(bar(s), kChunk);
-          bulk_load(smem_u32(smem + (2 * warp + s) * kChunk), src, kChunk, bar(s));
+          bulk_load(smem_u32(smem + (2 * warp + s) * kChunk),
+                    c.pool + ((int64_t)id * c.Hkv + next.head) * kChunk, kChunk, bar(s));
         } else {
           atomicOr(P.status, VS_DEVFLAG_BOUNDS);
           mbar_arrive(bar(s));
@@ -424,7 +454,7 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
       }
       if (++issued < pages) {
         cursor_add(P, next, 1);
-        src = source();  // used only when its slot is free
+        look_up();
       }
     };
     issue();
