@@ -556,7 +556,7 @@ vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64
  *            acc_out itself, or NULL (zeros).  ld >= max_len.  Entries from
  *            lens[b] on are left as they were.
  *   lse      fp32 [Hq][B] (output) or NULL.
- * The values' steps s are expected in [2^-40, 2^60] and |Q| below 2^113; beyond
+ * The values' steps s are expected in [2^-40, 2^40] and |Q| below 2^113; beyond
  * that results lose precision or overflow.
  * A sequence without slots gives O = 0 and LSE = -inf.  Results do not depend
  * on timing: repeated calls give the same bits on the same device.

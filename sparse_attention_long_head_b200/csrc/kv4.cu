@@ -12,8 +12,10 @@
 // n = 0; an infinity or NaN in the group gives s = m = NaN, so that the group
 // reads back as NaN.
 //
-// Both kernels are bound by memory: 4 d bytes of bf16 K and V and 9/8 d bytes
-// of cache per token and head.  Eight lanes take one group of one slot (16
+// The floor of both kernels is memory: 4 d bytes of bf16 K and V and 9/8 d bytes
+// of cache per token and head.  50,413 tokens of 8 heads, d = 128 (265 MB):
+// append 93 us, bound by instruction issue (3.3 of 4 a cycle, some 380 per warp
+// and 512 values), read 54 us, 4.9 TB/s.  Eight lanes take one group of one slot (16
 // bytes of K and of V each), so every access is a full 32- or 128-byte piece.
 #include <cuda_bf16.h>
 

@@ -17,8 +17,11 @@
 // that the rounding of p s to bf16, the only rounding below fp32, acts on
 // n - 8, as it would on the values themselves, and the running sums stay small.
 //
-// Bound by the cache's bytes: 72 per slot, KV head and group (64 codes and
-// pairs of K and V), at G = Hq / Hkv query heads each.  mma.sync m16n8k16 is
+// Its floor is the cache's bytes: 72 per slot, KV head and group (64 codes and
+// pairs of K and V), at G = Hq / Hkv query heads each.  4 x 128K slots, 32/8
+// heads, d = 128 take 110 us (5.3 TB/s, 80% of a copy); what bounds it there is
+// instructions, 217 per 16 slots: the ALU pipe is busy 54% of the cycles and
+// an issue slot 50%, with three warps a scheduler.  mma.sync m16n8k16 is
 // used, not tcgen05: with 8 or 16 columns of useful work (the query heads of
 // one KV head) the tensor rate is far from the bound, and operands made in
 // registers go straight in, without a trip through shared or tensor memory.
@@ -49,8 +52,9 @@ struct DecodeShape {
 };
 constexpr int kDecMaxWarps = 12;
 
-// The weights carry 2^kShift: V steps s from 2^-40 (below, the products with
-// codes of 2^-133 lose bits) to 2^60 (above, sums over long rows overflow).
+// The weights carry 2^kShift (up to 2^8 more while the running maximum lags):
+// V steps s from 2^-40 (below, the products with codes of 2^-133 lose bits) to
+// 2^40 (above, 2^56 15 s summed over 2^24 slots overflows).
 constexpr float kShift = 48.f;
 constexpr int kDecMinPages = 12;  // per CTA, where the list is short
 
@@ -899,7 +903,8 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
 
 // acc_out = acc_in + sum over the KV head's query heads of the softmax weight,
 // per slot; invisible slots keep their sum.  Bound by memory: a float per query
-// head and two for acc per slot.  W: floats of a score load (Gp is a multiple).
+// head and two for acc per slot; 236,000 slots of 8 heads (4 query heads each):
+// 16 us, 2.8 TB/s.  W: floats of a score load (Gp is a multiple).
 template <int W>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const float* acc_in,
                                                           float* acc_out, int64_t ld) {
