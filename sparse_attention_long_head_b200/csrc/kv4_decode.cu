@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const 
           *reinterpret_cast<float2*>(x) = __ldcs(reinterpret_cast<const float2*>(s + h));
 #pragma unroll
         for (int i = 0; i < W; ++i)
-          if (h + i < P.G) w += ex2_approx(x[i] - __ldg(lse2 + h + i));
+          if (h + i < P.G) w += ex2_approx(x[i] - __ldcg(lse2 + h + i));
       }
       sum += w;
     }

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kMoveThreads)
   wait_for_previous_kernel();
   const Kv4Cache& c = a.c;
   const int row = blockIdx.y, b = row / c.Hkv, head = row % c.Hkv;
-  const int moves = counts[row];
+  const int moves = __ldcg(counts + row);
   const int32_t* hole_list = lists + (int64_t)row * 2 * list_ld;
   const int32_t* mover_list = hole_list + list_ld;
   const int groups = gridDim.x * (kMoveThreads / 16);
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 #pragma unroll
     for (int u = 0; u < kMoves; ++u) {
       const int i = i0 + u * groups;
-      dst[u] = i < moves ? hole_list[i] : -1;
-      src[u] = i < moves ? mover_list[i] : -1;
+      dst[u] = i < moves ? __ldcg(hole_list + i) : -1;
+      src[u] = i < moves ? __ldcg(mover_list + i) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kMoves; ++u) {

@@ -536,6 +536,84 @@ def test_evict_flags_bad_lengths_and_pages(cuda_device):
     assert np.array_equal(po[1, 0, :100], src)
 
 
+def test_pool_beyond_32_bit_offsets(cuda_device):
+    """Pages behind the first 4 GiB of a pool: the same bytes and bits as in a small pool."""
+    rng = np.random.default_rng(31)
+    Hkv, d, n = 8, 128, 300
+    far = (5 << 30) // (Hkv * 9216)
+    big, small = vs.kv4_pool(far + 8, Hkv, d), vs.kv4_pool(8, Hkv, d)
+    K, V, Q = (_dev(ref.bf16_round(rng.standard_normal((m, h, d)))) for m, h in ((n, Hkv), (n, Hkv), (1, 32)))
+    acc = torch.rand((1, Hkv, n), device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, Hkv, n).contiguous()
+    ws = vs.workspace(1 << 24)
+    got = []
+    for pool, first in ((big, far), (small, 0)):
+        pool[first:].zero_()
+        table = torch.arange(5, dtype=torch.int32, device="cuda").view(1, 5) + first
+        vs.vs_kv4_append(K, V, _cu([n]), n, pool, table, _ints([n]), ws)
+        O, lse = vs.kv4_decode_attention(Q, pool, table, _ints([n]), n)
+        out = [_ints([0]), torch.zeros((1, Hkv, 100), device="cuda"),
+               torch.zeros((1, Hkv, 100), dtype=torch.int32, device="cuda")]
+        vs.vs_kv4_evict(pool, table, _ints([n]), _ints([n]), n, acc, pos, 100, 2, 9, *out, ws)
+        Kr, Vr = torch.zeros((100, Hkv, d), dtype=torch.bfloat16, device="cuda"), torch.zeros((100, Hkv, d), dtype=torch.bfloat16, device="cuda")
+        vs.vs_kv4_read(pool, table, out[0], None, _cu([100]), 100, Kr, Vr, ws)
+        assert vs.vs_read_device_status(ws) == (vs.VS_OK, 0)
+        got.append([O, lse, Kr, Vr, pool[first:].clone()] + out)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_captured_weights_and_eviction_replay_like_eager_calls(cuda_device):
+    """Decode with weights and evict (two kernels each) in one graph, replayed on a stream of its own while
+    another stream runs the same calls with a workspace and a cache of its own."""
+    rng = np.random.default_rng(33)
+    lens, Hq, Hkv, d, keep = [900, 64, 3000], 8, 2, 64, 800
+    B, top = len(lens), 3000
+    q, table, pool0 = _decode_case(rng, lens, Hq, Hkv, d)
+    Q, td, ln = _dev(q), torch.from_numpy(table).cuda(), _ints(lens)
+    pos = torch.arange(top, dtype=torch.int32, device="cuda").expand(B, Hkv, top).contiguous()
+    acc0 = torch.rand((B, Hkv, top), device="cuda")
+
+    class Side:
+        def __init__(self):
+            self.pool, self.acc = torch.from_numpy(pool0).cuda(), torch.zeros_like(acc0)
+            self.O, self.lse = torch.empty_like(Q), torch.empty((Hq, B), device="cuda")
+            self.out = [torch.zeros_like(ln), torch.zeros((B, Hkv, keep), device="cuda"),
+                        torch.zeros((B, Hkv, keep), dtype=torch.int32, device="cuda")]
+            self.ws = vs.workspace(max(vs.vs_kv4_decode_workspace_size(B, Hq, Hkv, d, top, True),
+                                       vs.vs_kv4_evict_workspace_size(B, Hkv, top, keep)))
+
+        def step(self):
+            vs.vs_kv4_decode_attn_fwd(Q, self.pool, td, ln, top, self.O, self.lse, self.ws, acc_in=acc0,
+                                      acc_out=self.acc)
+            vs.vs_kv4_evict(self.pool, td, ln, ln, top, self.acc, pos, keep, 4, 100, *self.out, self.ws)
+
+        def results(self):
+            return [self.O, self.lse, self.acc, self.pool] + self.out
+
+    a, b, eager = Side(), Side(), Side()
+    eager.pool.copy_(torch.from_numpy(pool0).cuda())
+    eager.step()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s1):
+            a.step()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for side in (a, b):
+            side.pool.copy_(torch.from_numpy(pool0).cuda())
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            graph.replay()
+        with torch.cuda.stream(s2):
+            b.step()
+        torch.cuda.synchronize()
+        for side in (a, b):
+            assert all(torch.equal(x, y) for x, y in zip(side.results(), eager.results()))
+            assert vs.vs_read_device_status(side.ws) == (vs.VS_OK, 0)
+
+
 # -------------------------------------------------------------------------------------- together
 
 
