@@ -1103,9 +1103,12 @@ static cudaError_t launch_tc_impl(const AttnArgs& a, const PlanLayout& L) {
   if (SPARSE && a.pack_vrows > 0) {  // packed vertical rows: [H_sel * vrows][D] tiles
     encode_map(enc, &mKg, a.pack_k, D, (int64_t)a.B * a.H_sel * a.pack_vrows, D, 128, &rc);
     encode_map(enc, &mVg, a.pack_v, D, (int64_t)a.B * a.H_sel * a.pack_vrows, D, 128, &rc);
-  } else {
+  } else if (SPARSE) {
     encode_map(enc, &mKg, a.K, (int64_t)a.Hkv * D, a.total, a.kv_stride, 1, &rc);
     encode_map(enc, &mVg, a.V, (int64_t)a.Hkv * D, a.total, a.kv_stride, 1, &rc);
+  } else {  // only the vertical-slash kernel reads these maps
+    mKg = mK;
+    mVg = mV;
   }
   if (rc != CUDA_SUCCESS) return cudaErrorInvalidValue;
   AttnParams P;

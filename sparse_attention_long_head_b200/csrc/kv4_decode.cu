@@ -829,17 +829,22 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
           make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
     if (lane == 0) write_lse(P, b, h, M, L);
   };
-  int turn = 0;
+  int turn = 0, wa = 0, wb = 0;
   for (int at = 0; at < count;) {
     const int k0 = seg.k, k1 = min(seg.v.pages, k0 + (count - at));
-    const int wa = at / wper, wb = (at + (k1 - k0) - 1) / wper;  // the warps with pages of it
+    // the warps with pages of it
+    while ((wa + 1) * wper <= at) ++wa;
+    while ((wb + 1) * wper < at + (k1 - k0)) ++wb;
     const bool shared = k0 > 0 || k1 < seg.v.pages;
     const int heads = min(HR, P.G - seg.hc * HR), h0 = seg.head * P.G + seg.hc * HR;
     if (shared || wa != wb) {
       // the CTA's part: its first row's or its last row's
       float* out = P.parts + (size_t)(2 * blockIdx.x + (at > 0 ? 1 : 0)) * kPart;
-      for (int h = 0; h < heads; ++h, ++turn) {
-        if (turn % kWarps != warp) continue;
+      // the heads go round the warps: this warp's first is the one at its turn
+      int h = warp - turn;
+      if (h < 0) h += kWarps;
+      turn = (turn + heads) % kWarps;
+      for (; h < heads; h += kWarps) {
         // a warp's part of the row is its first unless its range starts before the row
         auto part_of = [&](int w) {
           return P.warp_parts +
@@ -887,8 +892,10 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
   for (int x = 0; x < 2; ++x) {
     if (!s_last[x]) continue;
     const SharedRow sr = s_row[x];
-    for (int h = 0; h < sr.heads; ++h, ++turn) {
-      if (turn % kWarps != warp) continue;
+    int h = warp - turn;
+    if (h < 0) h += kWarps;
+    turn = (turn + sr.heads) % kWarps;
+    for (; h < sr.heads; h += kWarps) {
       // CTA x's part is its first unless its range starts before the row
       auto part_of = [&](int cta) {
         return P.parts + (size_t)(2 * cta + ((int64_t)cta * share < sr.start ? 1 : 0)) * kPart;
