@@ -15,10 +15,10 @@
 // histograms that the cluster sums through distributed shared memory, and
 // ballots in slot order give the lists of holes and of the slots that fill
 // them.  Bound by latency (some ten cluster barriers and the row read once, 8
-// bytes a slot).  The second moves, a few moves in flight per 16 lanes over
-// the whole device.  256 rows of 4352 slots cut to 4096 take 17 us and 13 us
-// (three dependent loads a move), 16 rows of 100,000 to 131,072 slots cut to
-// 8192 take 39 us and 29 us (123,000 moves of 144 bytes in pieces of 32 and 4).
+// bytes a slot).  The second moves, 16 lanes a move over the whole device.
+// 256 rows of 4352 slots cut to 4096 take 27 us, 16 rows of 100,000 to 131,072
+// slots cut to 8192 take 60 us (123,000 moves of 144 bytes in pieces of 32 and
+// 4); by themselves 16 and 16 (three dependent loads a move), 36 and 27.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
   // Boundary key: the k-th largest.  `need` slots are still to be found among
   // the `equal` ones whose key begins with `prefix`.
   uint32_t prefix = 0, need = k, equal = n;
+  int low = 32;  // bits below the digits found so far
   __syncthreads();  // the histograms are zero
 #pragma unroll
   for (int pass = 0; pass < 4; ++pass) {
@@ -182,8 +183,12 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
     prefix = (prefix << 8) | __shfl_sync(0xffffffffu, digit, from);
     equal = __shfl_sync(0xffffffffu, count, from);
     need -= __shfl_sync(0xffffffffu, above, from);
+    low = shift;
+    if (equal == need) break;  // uniform over the cluster: all that begin with prefix stay
   }
-  const uint32_t bound = prefix;  // `need` of the `equal` slots with this key stay, the lowest
+  // Larger keys stay, and `need` of the `equal` slots with this key, the lowest
+  // ones (all of them, from this key up, where the search ended early).
+  const uint32_t bound = prefix << low;
 
   // this warp's counts x, y -> the counts of all earlier warps of the cluster
   auto exchange = [&](uint32_t x, uint32_t y, uint32_t& before_x, uint32_t& before_y) {
@@ -290,11 +295,12 @@ __global__ void __launch_bounds__(kEvThreads, kEvThreads == 512 ? 2 : 1)
 }
 
 // The moves of row blockIdx.y: sixteen lanes a move (16-byte pieces of the
-// codes, the pairs, the entries of acc and pos), kMoves moves in flight.
+// codes, the pairs, the entries of acc and pos).  One move a lane and turn, as
+// many blocks as are resident at once: two moves in flight take the same, four
+// at half the threads 5% more, two or four times the blocks 2% and 5% more.
 constexpr int kMoveThreads = 256;
-constexpr int kMoves = 4;
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 8)
     kv4_move_kernel(Kv4EvictArgs a, const int32_t* counts, const int32_t* lists, int64_t list_ld) {
   wait_for_previous_kernel();
   const Kv4Cache& c = a.c;
@@ -313,54 +319,26 @@ __global__ void __launch_bounds__(kMoveThreads)
     off = kv4_pair_off(c.GR, (sub - codes) / c.GR, (sub - codes) % c.GR, 0);
     step = 4;
   }
-  for (int i0 = blockIdx.x * (kMoveThreads / 16) + threadIdx.x / 16; i0 < moves;
-       i0 += groups * kMoves) {
-    int dst[kMoves], src[kMoves];
-    uint8_t* pd[kMoves];
-    const uint8_t* ps[kMoves];
-#pragma unroll
-    for (int u = 0; u < kMoves; ++u) {
-      const int i = i0 + u * groups;
-      dst[u] = i < moves ? __ldcg(hole_list + i) : -1;
-      src[u] = i < moves ? __ldcg(mover_list + i) : -1;
+  for (int i = blockIdx.x * (kMoveThreads / 16) + threadIdx.x / 16; i < moves; i += groups) {
+    const int dst = __ldcg(hole_list + i), src = __ldcg(mover_list + i);
+    if (sub == 14) {
+      a.acc_out[(int64_t)row * a.ld_out + dst] = __ldg(a.acc_in + (int64_t)row * a.ld_in + src);
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < kMoves; ++u) {
-      pd[u] = dst[u] >= 0 ? kv4_page(c, b, dst[u] >> 6, head) : nullptr;
-      ps[u] = dst[u] >= 0 ? kv4_page(c, b, src[u] >> 6, head) : nullptr;
+    if (sub == 15) {
+      a.pos_out[(int64_t)row * a.ld_out + dst] = __ldg(a.pos_in + (int64_t)row * a.ld_in + src);
+      continue;
     }
-    uint4 x[kMoves];
-#pragma unroll
-    for (int u = 0; u < kMoves; ++u) {
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (dst[u] < 0) continue;
-      const int64_t at = (int64_t)row * a.ld_in + src[u];
-      if (sub == 14) {
-        x[u].x = __float_as_uint(__ldg(a.acc_in + at));
-      } else if (sub == 15) {
-        x[u].x = (uint32_t)__ldg(a.pos_in + at);
-      } else if (pd[u] && ps[u]) {
-        const uint8_t* p = ps[u] + off + step * (src[u] & 63);
-        if (step == 32) x[u] = *reinterpret_cast<const uint4*>(p);
-        else if (step == 4) x[u].x = *reinterpret_cast<const uint32_t*>(p);
-      } else if (sub == 0) {
-        atomicOr(static_cast<int*>(a.ws), VS_DEVFLAG_BOUNDS);
-      }
+    uint8_t* pd = kv4_page(c, b, dst >> 6, head);
+    const uint8_t* ps = kv4_page(c, b, src >> 6, head);
+    if (!pd || !ps) {
+      if (sub == 0) atomicOr(static_cast<int*>(a.ws), VS_DEVFLAG_BOUNDS);
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < kMoves; ++u) {
-      if (dst[u] < 0) continue;
-      const int64_t at = (int64_t)row * a.ld_out + dst[u];
-      if (sub == 14) {
-        a.acc_out[at] = __uint_as_float(x[u].x);
-      } else if (sub == 15) {
-        a.pos_out[at] = (int)x[u].x;
-      } else if (pd[u] && ps[u]) {
-        uint8_t* p = pd[u] + off + step * (dst[u] & 63);
-        if (step == 32) *reinterpret_cast<uint4*>(p) = x[u];
-        else if (step == 4) *reinterpret_cast<uint32_t*>(p) = x[u].x;
-      }
-    }
+    pd += off + step * (dst & 63);
+    ps += off + step * (src & 63);
+    if (step == 32) *reinterpret_cast<uint4*>(pd) = *reinterpret_cast<const uint4*>(ps);
+    else if (step == 4) *reinterpret_cast<uint32_t*>(pd) = *reinterpret_cast<const uint32_t*>(ps);
   }
 }
 
@@ -415,8 +393,8 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a) {
   else if (C * 16384 >= n) e = launch_evict_impl<512, 32>(a, C, counts, lists, list);
   else e = launch_evict_impl<1024, 32>(a, C, counts, lists, list);
   if (e != cudaSuccess || list == 0) return e;
-  const int64_t per_block = (kMoveThreads / 16) * kMoves;
-  const int64_t want = (list + per_block - 1) / per_block, cap = ceil_div(16LL * sms, rows);
+  const int64_t per_block = kMoveThreads / 16;
+  const int64_t want = (list + per_block - 1) / per_block, cap = ceil_div(8LL * sms, rows);
   return launch_after(kv4_move_kernel, dim3((unsigned)(want < cap ? want : cap), rows),
                       kMoveThreads, a.stream, a, (const int*)counts, (const int*)lists, list);
 }
