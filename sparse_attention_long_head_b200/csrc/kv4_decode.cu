@@ -911,11 +911,15 @@ __global__ void __launch_bounds__(DecodeShape<NT>::kThreads, 1)
 // acc_out = acc_in + sum over the KV head's query heads of the softmax weight,
 // per slot; invisible slots keep their sum.  Bound by memory: a float per query
 // head and two for acc per slot; 236,000 slots of 8 heads (4 query heads each):
-// 16 us, 2.8 TB/s.  W: floats of a score load (Gp is a multiple).
+// 14 us, 3.2 TB/s.  Two slots a thread, so that their loads overlap: one or four
+// take 2 us longer.  W: floats of a score load (Gp is a multiple).
+constexpr int kWeightsTurn = 512;  // slots of a block and turn
 template <int W>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const float* acc_in,
                                                           float* acc_out, int64_t ld) {
-  wait_for_previous_kernel();
+  constexpr int kSlots = kWeightsTurn / 256;
+  constexpr int kHeads = 128;  // log-sum-exps kept; a load per slot for further heads
+  __shared__ float s_lse2[kHeads];
   const Kv4Cache& c = P.c;
   const int b = blockIdx.y / c.Hkv, head = blockIdx.y % c.Hkv;
   int n;
@@ -923,24 +927,41 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(DecodeParams P, const 
   const int lo_slot = P.window > 0 && n > P.window ? n - P.window : 0;
   const float* lse2 = P.lse2 + (int64_t)b * P.Hq + (int64_t)head * P.G;
   const int64_t row = (int64_t)b * c.Hkv + head;
-  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x) {
-    float sum = acc_in ? acc_in[row * ld + t] : 0.f;
-    if ((t >= lo_slot || t < P.sinks) && kv4_page(c, b, t >> 6, head)) {
-      const float* s = P.score + (row * P.slots + t) * P.Gp;
-      float w = 0.f;
-      for (int h = 0; h < P.G; h += W) {
-        float x[W];
-        if constexpr (W == 4)
-          *reinterpret_cast<float4*>(x) = __ldcs(reinterpret_cast<const float4*>(s + h));
-        else
-          *reinterpret_cast<float2*>(x) = __ldcs(reinterpret_cast<const float2*>(s + h));
+  wait_for_previous_kernel();
+  if (threadIdx.x < P.G && threadIdx.x < kHeads) s_lse2[threadIdx.x] = __ldcg(lse2 + threadIdx.x);
+  __syncthreads();
+  for (int t0 = blockIdx.x * kWeightsTurn + threadIdx.x; t0 < n; t0 += gridDim.x * kWeightsTurn) {
+    float sum[kSlots], w[kSlots] = {};
+    bool seen[kSlots];
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-          if (h + i < P.G) w += ex2_approx(x[i] - __ldcg(lse2 + h + i));
-      }
-      sum += w;
+    for (int u = 0; u < kSlots; ++u) {
+      const int t = t0 + 256 * u;
+      sum[u] = acc_in && t < n ? acc_in[row * ld + t] : 0.f;
+      seen[u] = t < n && (t >= lo_slot || t < P.sinks) && kv4_page(c, b, t >> 6, head);
     }
-    acc_out[row * ld + t] = sum;
+    for (int h = 0; h < P.G; h += W) {
+      float x[kSlots][W] = {};
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) {
+        const int t = t0 + 256 * u;
+        if (t >= n) continue;
+        const float* s = P.score + (row * P.slots + t) * P.Gp + h;
+        if constexpr (W == 4)
+          *reinterpret_cast<float4*>(x[u]) = __ldcs(reinterpret_cast<const float4*>(s));
+        else
+          *reinterpret_cast<float2*>(x[u]) = __ldcs(reinterpret_cast<const float2*>(s));
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (h + i >= P.G) continue;
+        const float l = h + i < kHeads ? s_lse2[h + i] : __ldcg(lse2 + h + i);
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) w[u] += ex2_approx(x[u][i] - l);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u)
+      if (t0 + 256 * u < n) acc_out[row * ld + t0 + 256 * u] = seen[u] ? sum[u] + w[u] : sum[u];
   }
 }
 
@@ -1003,7 +1024,7 @@ cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a) {
     e = a.c.GR == 1 ? launch_decode_impl<1, 2, false>(P, grid, a.stream)
                     : launch_decode_impl<2, 2, false>(P, grid, a.stream);
   if (e != cudaSuccess || !a.acc_out) return e;
-  const int64_t per_row = (L.slots + 255) / 256;
+  const int64_t per_row = (L.slots + kWeightsTurn - 1) / kWeightsTurn;
   const int64_t cap = ceil_div(32LL * sms, a.c.B * a.c.Hkv);
   const dim3 wgrid((unsigned)(per_row < cap ? per_row : cap), a.c.B * a.c.Hkv);
   return launch_after(L.Gp % 4 == 0 ? kv4_weights_kernel<4> : kv4_weights_kernel<2>, wgrid, 256,
