@@ -14,8 +14,8 @@
 //
 // The floor of both kernels is memory: 4 d bytes of bf16 K and V and 9/8 d bytes
 // of cache per token and head.  50,413 tokens of 8 heads, d = 128 (265 MB):
-// append 93 us, bound by instruction issue (3.3 of 4 a cycle, some 380 per warp
-// and 512 values), read 54 us, 4.9 TB/s.  Eight lanes take one group of one slot (16
+// append 90 us, bound by instruction issue (3.2 of 4 a cycle, some 370 per warp
+// and 512 values; the ALU pipe at 69%), read 54 us, 4.9 TB/s.  Eight lanes take one group of one slot (16
 // bytes of K and of V each), so every access is a full 32- or 128-byte piece.
 #include <cuda_bf16.h>
 
@@ -46,6 +46,29 @@ __device__ __forceinline__ __nv_bfloat162 abs2(uint32_t a) {
 }
 __device__ __forceinline__ float bf16_at(const uint32_t (&v)[4], int i) {
   return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+}
+
+// Two fp32 in one register pair; one instruction for both (append 93 -> 90 us).
+__device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) {
+  return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t both(float x) {
+  return pair2(__float_as_uint(x), __float_as_uint(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Adding this to x in [0, 2^22) leaves rint(x) in the low bits.
@@ -91,12 +114,14 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
     for (int i = 0; i < 8; ++i) exact &= fabsf(bf16_at(v, i)) >= tiny || bf16_at(v, i) == 0.f;
   }
   const float r = __fdividef(1.f, s);  // to 2^-22
+  const uint64_t r2 = both(r), minus_s = both(-s), minus_lo = both(-lo), round2 = both(kRound);
   uint32_t word = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float d = bf16_at(v, i) - lo, q = d * r;
-    const float x = fmaf(fmaf(-q, s, d), r, q) + kRound;  // below 15.1
-    word = word * 16u + __float_as_uint(x);
+  for (int i = 3; i >= 0; --i) {
+    const uint64_t d = add2(pair2(v[i] << 16, v[i] & 0xffff0000u), minus_lo);
+    const uint64_t q = mul2(d, r2);
+    const uint64_t x = add2(fma2(fma2(q, minus_s, d), r2, q), round2);  // below 15.1
+    word = (word * 16u + (uint32_t)(x >> 32)) * 16u + (uint32_t)x;
   }
   word -= kRoundBits * 0x11111111u;  // of all eight
   if (!exact) {  // quotients next to a half, or overflowed, in 64 bits
