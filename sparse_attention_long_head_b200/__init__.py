@@ -188,6 +188,17 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _stream_at(stream, *tensors):
+    """The stream of a call whose tensors must be on the current device."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != device:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{device}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
+
+
 def _dtype(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return VS_BF16
@@ -289,17 +300,24 @@ def vs_dense_attn_fwd(Q, K, V, O, lse, ws, softmax_scale=0.0, stream=None):
            "vs_dense_attn_fwd")
 
 
+def _window_args(Q, K, V, O, lse):
+    N, Hq, d = Q.shape
+    assert O.shape == Q.shape and V.shape == K.shape and K.shape[::2] == (N, d)
+    for t, like in ((Q, None), (O, Q), (K, None), (V, K)):
+        _rows(t, like)
+    assert lse is None or _is(lse, torch.float32, (Hq, N))
+
+
 def vs_window_attn_fwd(Q, K, V, window, sinks, O, lse, ws, softmax_scale=0.0, stream=None):
     """Sliding window of `window` keys with the first `sinks` keys visible; lse fp32 [Hq, N] or
     None; ws of 256 bytes."""
     N, Hq, d = Q.shape
     Hkv = K.shape[1]
-    for t, like in ((Q, None), (O, Q), (K, None), (V, K)):
-        _rows(t, like)
+    _window_args(Q, K, V, O, lse)
     _check(lib().vs_window_attn_fwd(_ptr(Q), _ptr(K), _ptr(V), _dtype(Q), N, Hq, Hkv, d,
                                     Q.stride(0), K.stride(0), float(softmax_scale), int(window),
                                     int(sinks), _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "vs_window_attn_fwd")
+                                    _stream_at(stream, Q, K, V, O, ws)), "vs_window_attn_fwd")
 
 
 def vs_window_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, window, sinks, O, lse, ws,
@@ -307,12 +325,13 @@ def vs_window_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, window, sinks, O,
     T, Hq, d = Q.shape
     Hkv = K.shape[1]
     B = cu_seqlens.numel() - 1
-    for t, like in ((Q, None), (O, Q), (K, None), (V, K)):
-        _rows(t, like)
+    _window_args(Q, K, V, O, lse)
+    _ints(cu_seqlens)
     _check(lib().vs_window_attn_fwd_varlen(
         _ptr(Q), _ptr(K), _ptr(V), _dtype(Q), T, B, _ptr(cu_seqlens), int(max_seqlen), Hq, Hkv, d,
         Q.stride(0), K.stride(0), float(softmax_scale), int(window), int(sinks), _ptr(O),
-        _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "vs_window_attn_fwd_varlen")
+        _ptr(lse), _ptr(ws), ws.numel(), _stream_at(stream, Q, K, V, O, cu_seqlens, ws)),
+        "vs_window_attn_fwd_varlen")
 
 
 def vs_attn_aggregate(Q, K, lse, A_v, A_s, ws, softmax_scale=0.0, stream=None):
@@ -475,31 +494,50 @@ def vs_kv4_evict_workspace_size(B: int, Hkv: int, max_len: int, keep: int) -> in
     return int(lib().vs_kv4_evict_workspace_size(B, Hkv, max_len, keep))
 
 
+def _is(t, dtype, shape):
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _ints(t, n=0):
+    """Checks an int32 vector of at least n entries, or None."""
+    assert t is None or (t.dtype is _int32 and t.numel() >= n and t.is_contiguous())
+
+
 def _rows(t, like=None):
-    """Checks [tokens, heads, d] with packed heads (and the row stride of `like`)."""
+    """Checks [tokens, heads, d] with packed heads (and the row stride and type of `like`)."""
     _, H, d = t.shape
-    st = t.stride()
-    assert st[2] == 1 and (H == 1 or st[1] == d), "heads of a row must be contiguous"
-    assert like is None or (t.dtype == like.dtype and st[0] == like.stride(0)), "rows must match"
+    s0, s1, s2 = t.stride()
+    assert s2 == 1 and (H == 1 or s1 == d), "heads of a row must be contiguous"
+    assert like is None or (t.dtype is like.dtype and s0 == like.stride(0)), "rows must match"
 
 
+def _kv_rows(K, V, Hkv, d):
+    """Checks K and V [tokens, Hkv, d] of one layout."""
+    _, h, dk = K.shape
+    assert h == Hkv and dk == d and V.shape == K.shape and V.dtype is K.dtype
+    _rows(K)
+    if V.stride() != K.stride():
+        _rows(V, K)
+
+
+_int32, _float32 = torch.int32, torch.float32
 _KV4_HEAD_DIM = {4608: 64, 9216: 128}  # bytes per page and head -> d
 
 
 def _kv4_dims(pool):
     """(n_pages, Hkv, d) of a pool [n_pages, Hkv, bytes]."""
     n_pages, Hkv, nbytes = pool.shape
-    assert pool.dtype == torch.uint8 and pool.is_contiguous()
+    assert pool.dtype is torch.uint8 and pool.is_contiguous()
     d = _KV4_HEAD_DIM.get(nbytes)
     if d is None:
         raise ValueError(f"{nbytes} bytes per page and head are no cache format")
     return n_pages, Hkv, d
 
 
-def _kv4_max(table, lens, max_len=None):
+def _kv4_max(table, lens, B, max_len=None):
     """The bound on lengths that a page table [B, pages] gives, checked against the caller's."""
-    assert table.dtype == lens.dtype == torch.int32 and table.stride(1) == 1
-    assert table.shape[0] >= lens.numel() and lens.is_contiguous()
+    assert table.dtype is _int32 and table.stride(1) == 1 and table.shape[0] >= B
+    _ints(lens, B)
     room = min(64 * table.shape[1], 1 << 24)
     if max_len is None:
         return room
@@ -508,13 +546,15 @@ def _kv4_max(table, lens, max_len=None):
     return max_len
 
 
-def _kv4_rows(t):
-    """Row length of an acc or pos tensor [B, Hkv, ld] (its rows may be a slice of longer ones)."""
-    B, Hkv, ld = t.shape
+def _kv4_rows(t, dtype, B, Hkv, need=0):
+    """Row length of an acc or pos tensor [B, Hkv, ld]; its rows may be a slice, of at least
+    `need` entries, of longer ones."""
+    b, h, ld = t.shape
+    assert t.dtype is dtype and b == B and h == Hkv
     if t.is_contiguous():
         return ld
     sb, sh, s1 = t.stride()
-    assert (ld <= 1 or s1 == 1) and (B <= 1 or sb == Hkv * sh)
+    assert need <= ld <= sh and (ld <= 1 or s1 == 1) and (B <= 1 or sb == Hkv * sh)
     return sh if B * Hkv > 1 else ld
 
 
@@ -524,33 +564,41 @@ def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=Non
     [B, pages]; lens int32 [B], the new tokens included; acc fp32 and pos int32 [B, Hkv, ld]."""
     T = K.shape[0]
     n_pages, Hkv, d = _kv4_dims(pool)
-    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape
-    _rows(K)
-    _rows(V, K)
+    _kv_rows(K, V, Hkv, d)
     B = cu_seqlens.numel() - 1
-    rows = acc if acc is not None else pos
-    ld = 0 if rows is None else _kv4_rows(rows)
-    assert acc is None or pos is None or _kv4_rows(pos) == ld
+    _ints(cu_seqlens)
+    _ints(n_tokens, B)
+    ld, max_len = 0, _kv4_max(table, lens, B)
+    if acc is not None:
+        ld = _kv4_rows(acc, _float32, B, Hkv)
+        max_len = min(max_len, acc.shape[2])
+    if pos is not None:
+        ld_pos = _kv4_rows(pos, _int32, B, Hkv)
+        assert acc is None or ld_pos == ld
+        ld, max_len = ld_pos, min(max_len, pos.shape[2])
     Hq = A_v.shape[0] if A_v is not None else Hkv
-    assert A_v is None or (A_v.shape[1] == T and A_v.is_contiguous())
+    assert A_v is None or _is(A_v, _float32, (Hq, T))
     _check(lib().vs_kv4_append(_ptr(K), _ptr(V), _dtype(K), T, _ptr(cu_seqlens), int(max_new),
                                K.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
-                               _ptr(lens), _ptr(n_tokens), B, _kv4_max(table, lens), Hq, Hkv, d,
+                               _ptr(lens), _ptr(n_tokens), B, max_len, Hq, Hkv, d,
                                _ptr(A_v), _ptr(acc), _ptr(pos), ld, _ptr(ws), ws.numel(),
-                               _stream(stream)), "vs_kv4_append")
+                               _stream_at(stream, K, V, pool, table, lens, ws)), "vs_kv4_append")
 
 
 def vs_kv4_read(pool, table, lens, start, cu_seqlens, max_read, K, V, ws, stream=None):
     """Slots [start[b], start[b] + n_b) into rows [cu[b], cu[b + 1]) of K, V [T, Hkv, d] bf16;
     start int32 [B] or None."""
     n_pages, Hkv, d = _kv4_dims(pool)
-    assert K.shape[1:] == (Hkv, d) and V.shape == K.shape and K.dtype == torch.bfloat16
-    _rows(K)
-    _rows(V, K)
+    assert K.dtype is torch.bfloat16
+    _kv_rows(K, V, Hkv, d)
+    B = cu_seqlens.numel() - 1
+    _ints(cu_seqlens)
+    _ints(start, B)
     _check(lib().vs_kv4_read(_ptr(pool), n_pages, _ptr(table), table.stride(0), _ptr(lens),
-                             _ptr(start), cu_seqlens.numel() - 1, _kv4_max(table, lens), Hkv, d,
+                             _ptr(start), B, _kv4_max(table, lens, B), Hkv, d,
                              _ptr(cu_seqlens), int(max_read), K.shape[0], _ptr(K), _ptr(V),
-                             K.stride(0), _ptr(ws), ws.numel(), _stream(stream)), "vs_kv4_read")
+                             K.stride(0), _ptr(ws), ws.numel(),
+                             _stream_at(stream, K, V, pool, table, lens, ws)), "vs_kv4_read")
 
 
 def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, sinks=0,
@@ -561,13 +609,14 @@ def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, 
     assert dp == d and O.shape == Q.shape
     _rows(Q)
     _rows(O, Q)
-    ld = 0 if acc_out is None else _kv4_rows(acc_out)
-    assert acc_in is None or acc_out is None or _kv4_rows(acc_in) == ld
+    assert lse is None or _is(lse, _float32, (Hq, B))
+    ld = 0 if acc_out is None else _kv4_rows(acc_out, _float32, B, Hkv, max_len)
+    assert acc_in is None or _kv4_rows(acc_in, _float32, B, Hkv, max_len) == ld
     _check(lib().vs_kv4_decode_attn_fwd(
         _ptr(Q), _dtype(Q), Q.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
-        _ptr(lens), B, _kv4_max(table, lens, max_len), Hq, Hkv, d, float(softmax_scale), int(window),
+        _ptr(lens), B, _kv4_max(table, lens, B, max_len), Hq, Hkv, d, float(softmax_scale), int(window),
         int(sinks), _ptr(acc_in), _ptr(acc_out), ld, _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
-        _stream(stream)), "vs_kv4_decode_attn_fwd")
+        _stream_at(stream, Q, O, pool, table, lens, ws)), "vs_kv4_decode_attn_fwd")
 
 
 def vs_kv4_evict(pool, table, lens, n_tokens, max_len, acc, pos, keep, sinks, recent, lens_out,
@@ -575,13 +624,19 @@ def vs_kv4_evict(pool, table, lens, n_tokens, max_len, acc, pos, keep, sinks, re
     """acc fp32 and pos int32 [B, Hkv, ld]; lens_out int32 [B]; acc_out, pos_out [B, Hkv, ld_out]."""
     n_pages, Hkv, d = _kv4_dims(pool)
     B = lens.numel()
-    ld, ld_out = _kv4_rows(acc), _kv4_rows(acc_out)
-    assert _kv4_rows(pos) == ld and _kv4_rows(pos_out) == ld_out
+    kept = min(keep, max_len)
+    ld = _kv4_rows(acc, _float32, B, Hkv, max_len)
+    ld_out = _kv4_rows(acc_out, _float32, B, Hkv, kept)
+    assert _kv4_rows(pos, _int32, B, Hkv, max_len) == ld
+    assert _kv4_rows(pos_out, _int32, B, Hkv, kept) == ld_out
+    _ints(n_tokens, B)
+    _ints(lens_out, B)
     _check(lib().vs_kv4_evict(_ptr(pool), n_pages, _ptr(table), table.stride(0), _ptr(lens),
-                              _ptr(n_tokens), B, _kv4_max(table, lens, max_len), Hkv, d, _ptr(acc), _ptr(pos), ld,
+                              _ptr(n_tokens), B, _kv4_max(table, lens, B, max_len), Hkv, d,
+                              _ptr(acc), _ptr(pos), ld,
                               int(keep), int(sinks), int(recent), _ptr(lens_out), _ptr(acc_out),
-                              _ptr(pos_out), ld_out, _ptr(ws), ws.numel(), _stream(stream)),
-           "vs_kv4_evict")
+                              _ptr(pos_out), ld_out, _ptr(ws), ws.numel(),
+                              _stream_at(stream, pool, table, lens, acc, pos, ws)), "vs_kv4_evict")
 
 
 def vs_read_device_status(ws, stream=None) -> tuple[int, int]:

@@ -15,8 +15,9 @@
 // The floor of both kernels is memory: 4 d bytes of bf16 K and V and 9/8 d bytes
 // of cache per token and head.  50,413 tokens of 8 heads, d = 128 (265 MB):
 // append 90 us, bound by instruction issue (3.2 of 4 a cycle, some 370 per warp
-// and 512 values; the ALU pipe at 69%), read 54 us, 4.9 TB/s.  Eight lanes take one group of one slot (16
-// bytes of K and of V each), so every access is a full 32- or 128-byte piece.
+// and 512 values; the ALU pipe at 69%), read 54 us, 4.9 TB/s.  Eight
+// lanes take one group of one slot (16 bytes of K and of V each), so every access
+// is a full 32- or 128-byte piece.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"

@@ -142,3 +142,42 @@ def test_page_bytes_and_binding_checks():
     with pytest.raises(ValueError):
         vs.vs_kv4_decode_attn_fwd(q, torch.zeros((3, 2, 100), dtype=torch.uint8), table, table[:, 0].contiguous(), 256, q, None,
                                   vs.workspace(256, "cpu"))
+
+
+def test_binding_checks_types_and_shapes():
+    """What would be read or written out of range is refused before the call."""
+    table, lens = torch.zeros((2, 4), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    pool, ws = vs.kv4_pool(3, 2, 64, device="cpu"), vs.workspace(1 << 20, "cpu")
+    q, kv = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros((5, 2, 64), dtype=torch.bfloat16)
+    cu = torch.zeros(3, dtype=torch.int32)
+    acc, pos = torch.zeros((2, 2, 256)), torch.zeros((2, 2, 256), dtype=torch.int32)
+    for kw in (dict(lse=torch.zeros((2, 4))), dict(lse=torch.zeros((4, 2), dtype=torch.float64)),
+               dict(acc_out=acc[:1]), dict(acc_out=acc.double()), dict(acc_out=acc[..., :255]), dict(acc_out=acc, acc_in=acc[:, :1]),
+               dict(lens=lens[:1]), dict(lens=lens.long()), dict(table=table[:1])):
+        a = dict(lens=lens, table=table, lse=None, acc_in=None, acc_out=None) | kw
+        with pytest.raises(AssertionError):
+            vs.vs_kv4_decode_attn_fwd(q, pool, a["table"], a["lens"], 256, q.clone(), a["lse"], ws,
+                                      acc_in=a["acc_in"], acc_out=a["acc_out"])
+    for kw in (dict(acc=acc[:1]), dict(pos=pos[:, :1]), dict(acc=pos), dict(pos=pos.long()), dict(cu=cu.long()),
+               dict(n_tokens=lens[:1]), dict(A_v=torch.zeros((4, 4)), acc=acc), dict(lens=lens[:1])):
+        a = dict(cu=cu, lens=lens, n_tokens=None, A_v=None, acc=None, pos=None) | kw
+        with pytest.raises(AssertionError):
+            vs.vs_kv4_append(kv, kv, a["cu"], 5, pool, table, a["lens"], ws, n_tokens=a["n_tokens"], A_v=a["A_v"],
+                             acc=a["acc"], pos=a["pos"])
+    with pytest.raises(AssertionError):
+        vs.vs_kv4_read(pool, table, lens, lens[:1], cu, 5, kv, kv.clone(), ws)
+    for kw in (dict(acc=acc[:1]), dict(pos=acc), dict(lens_out=lens[:1]), dict(acc_out=acc[:, :1]),
+               dict(pos_out=pos[..., :99]), dict(acc=acc[..., :255]), dict(n_tokens=lens.long())):
+        a = dict(n_tokens=lens, acc=acc, pos=pos, lens_out=lens.clone(), acc_out=acc.clone(), pos_out=pos.clone()) | kw
+        with pytest.raises(AssertionError):
+            vs.vs_kv4_evict(pool, table, lens, a["n_tokens"], 256, a["acc"], a["pos"], 100, 4, 50, a["lens_out"],
+                            a["acc_out"], a["pos_out"], ws)
+
+
+def test_window_binding_checks_shapes():
+    q, k = torch.zeros((8, 4, 64), dtype=torch.bfloat16), torch.zeros((8, 2, 64), dtype=torch.bfloat16)
+    ws = vs.workspace(256, "cpu")
+    for args in ((q, k[:7], k[:7], q.clone(), None), (q, k, k[:, :1], q.clone(), None), (q, k, k, q[:7].clone(), None),
+                 (q, k, k, q.clone(), torch.zeros((8, 4))), (q, k, k, q.clone(), torch.zeros((4, 7)))):
+        with pytest.raises(AssertionError):
+            vs.vs_window_attn_fwd(*args[:3], 5, 1, *args[3:], ws)

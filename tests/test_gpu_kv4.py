@@ -319,6 +319,44 @@ def test_decode_same_bits_from_cold_and_warm_caches(Hq, d, weights, cuda_device)
     assert vs.vs_read_device_status(ws) == (vs.VS_OK, 0)
 
 
+@pytest.mark.parametrize("Hq,window,sinks", [(131, 0, 0), (260, 150, 70), (130, 0, 0)])
+def test_decode_weights_of_many_heads_per_kv_head(Hq, window, sinks, cuda_device):
+    rng = np.random.default_rng(Hq)
+    lens, Hkv, d = [1300, 1, 700], 2 if Hq == 260 else 1, 64
+    q, table, pool = _decode_case(rng, lens, Hq, Hkv, d)
+    Q, pd, td, ln = _dev(q), torch.from_numpy(pool).cuda(), torch.from_numpy(table).cuda(), _ints(lens)
+    ws = vs.workspace(vs.vs_kv4_decode_workspace_size(3, Hq, Hkv, d, 1300, True))
+    acc0 = rng.uniform(0, 1, (3, Hkv, 1301)).astype(np.float32)
+    acc = torch.from_numpy(acc0).cuda()
+    O, lse = torch.empty_like(Q), torch.empty((Hq, 3), device="cuda")
+    vs.vs_kv4_decode_attn_fwd(Q, pd, td, ln, 1300, O, lse, ws, window, sinks, acc_in=acc, acc_out=acc)
+    assert vs.vs_read_device_status(ws) == (vs.VS_OK, 0)
+    # the weights' sums have Hq / Hkv terms, so their rounding is counted per unit of the sum
+    w0 = acc.cpu().numpy().astype(np.float64) - acc0
+    assert np.abs(w0.sum(-1) - Hq // Hkv).max() <= 4e-4 * Hq // Hkv + 1301 * 2.0 ** -20
+    _check_decode(O, lse, q, pool, table, lens, window, sinks)
+    c = ref.Cache(pool)
+    for b, n in enumerate(lens):
+        w = ref.decode(q[b], c, table[b], n, window, sinks)[2]
+        # fp32 sums of up to 130 terms, then onto a sum of at most 131: half a unit in the last place each
+        assert (np.abs(w0[b, :, :n] - w) <= (4e-4 + 131 * 2.0 ** -24) * w + 2.0 ** -16).all(), b
+
+
+def test_tensors_of_another_device_are_refused(cuda_device):
+    pool, table, lens = vs.kv4_pool(2, 1, 64), torch.zeros((1, 2), dtype=torch.int32, device="cuda"), _ints([3])
+    Q = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    ws = vs.workspace(vs.vs_kv4_decode_workspace_size(1, 2, 1, 64, 128))
+    for bad in range(4):
+        args = [x.cpu() if i == bad else x for i, x in enumerate((Q, pool, table, lens))]
+        with pytest.raises(ValueError):
+            vs.vs_kv4_decode_attn_fwd(*args, 128, torch.empty_like(Q), None, ws)
+    K = Q[:, :1].contiguous()
+    with pytest.raises(ValueError):
+        vs.vs_kv4_append(K.cpu(), K.cpu(), _cu([1]), 1, pool, table, lens, ws)
+    with pytest.raises(ValueError):
+        vs.vs_window_attn_fwd(Q, K.cpu(), K.cpu(), 4, 1, torch.empty_like(Q), None, ws)
+
+
 def test_decode_many_short_sequences(cuda_device):
     rng = np.random.default_rng(8)
     lens = [int(x) for x in rng.integers(0, 130, 700)]
