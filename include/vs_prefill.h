@@ -475,7 +475,7 @@ vs_status vs_attn_aggregate_varlen(const void* Q, const void* K, vs_dtype dtype,
  * are in page table[b * table_ld + i].  Entries of pages that a call need not
  * touch are not read and may hold anything.  An entry outside [0, n_pages)
  * that is touched sets VS_DEVFLAG_BOUNDS; its slots are not written, or count
- * as invisible.
+ * as invisible.  Sequences may share pages that no call writes.
  * lens: int32 [B] (device), slots in use, the same for every head of a
  * sequence.  max_len (host) bounds them: 1 <= max_len <= 2^24, and at most
  * 64 table_ld.  A length outside [0, max_len] counts as 0 and sets
