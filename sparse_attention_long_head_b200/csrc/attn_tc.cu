@@ -431,8 +431,8 @@ __device__ __forceinline__ UnitInfo unit_info(const AttnParams& P, int u) {
     return ui;
   }
   if (MODE == kAttnWindow) {
-    // 32K tokens, 32/8 heads, d = 128, window 2048: 1.27 ms, 839 TFLOP/s of
-    // visible pairs (890 of computed tiles; the dense mode reaches 1140 on its
+    // 32K tokens, 32/8 heads, d = 128, window 2048: 1.27 ms, 842 TFLOP/s of
+    // visible pairs (893 of computed tiles; the dense mode reaches 1140 on its
     // long units, whose start and end weigh less).
     // the key blocks of the sinks below the window, then every block from the
     // first row's window to the diagonal

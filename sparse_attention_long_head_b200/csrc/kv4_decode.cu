@@ -19,7 +19,7 @@
 //
 // Its floor is the cache's bytes: 72 per slot, KV head and group (64 codes and
 // pairs of K and V), at G = Hq / Hkv query heads each.  4 x 128K slots, 32/8
-// heads, d = 128 take 110 us (5.3 TB/s, 80% of a copy); what bounds it there is
+// heads, d = 128 take 109 us (5.3 TB/s, 81% of a copy); what bounds it there is
 // instructions, 217 per 16 slots: the ALU pipe is busy 54% of the cycles and
 // an issue slot 50%, with three warps a scheduler.  mma.sync m16n8k16 is
 // used, not tcgen05: with 8 or 16 columns of useful work (the query heads of
