@@ -189,10 +189,11 @@ def _stream(stream):
 
 
 def _stream_at(stream, *tensors):
-    """The stream of a call whose tensors must be on the current device."""
+    """The stream of a call whose tensors (or None) must be on the current device: their addresses
+    go to a kernel as they are."""
     device = torch.cuda.current_device()
     for t in tensors:
-        if t.get_device() != device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{device}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
@@ -317,7 +318,7 @@ def vs_window_attn_fwd(Q, K, V, window, sinks, O, lse, ws, softmax_scale=0.0, st
     _check(lib().vs_window_attn_fwd(_ptr(Q), _ptr(K), _ptr(V), _dtype(Q), N, Hq, Hkv, d,
                                     Q.stride(0), K.stride(0), float(softmax_scale), int(window),
                                     int(sinks), _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
-                                    _stream_at(stream, Q, K, V, O, ws)), "vs_window_attn_fwd")
+                                    _stream_at(stream, Q, K, V, O, lse, ws)), "vs_window_attn_fwd")
 
 
 def vs_window_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, window, sinks, O, lse, ws,
@@ -330,7 +331,7 @@ def vs_window_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, window, sinks, O,
     _check(lib().vs_window_attn_fwd_varlen(
         _ptr(Q), _ptr(K), _ptr(V), _dtype(Q), T, B, _ptr(cu_seqlens), int(max_seqlen), Hq, Hkv, d,
         Q.stride(0), K.stride(0), float(softmax_scale), int(window), int(sinks), _ptr(O),
-        _ptr(lse), _ptr(ws), ws.numel(), _stream_at(stream, Q, K, V, O, cu_seqlens, ws)),
+        _ptr(lse), _ptr(ws), ws.numel(), _stream_at(stream, Q, K, V, O, lse, cu_seqlens, ws)),
         "vs_window_attn_fwd_varlen")
 
 
@@ -582,7 +583,8 @@ def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=Non
                                K.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
                                _ptr(lens), _ptr(n_tokens), B, max_len, Hq, Hkv, d,
                                _ptr(A_v), _ptr(acc), _ptr(pos), ld, _ptr(ws), ws.numel(),
-                               _stream_at(stream, K, V, pool, table, lens, ws)), "vs_kv4_append")
+                               _stream_at(stream, K, V, cu_seqlens, pool, table, lens, n_tokens, A_v, acc,
+                                          pos, ws)), "vs_kv4_append")
 
 
 def vs_kv4_read(pool, table, lens, start, cu_seqlens, max_read, K, V, ws, stream=None):
@@ -598,7 +600,8 @@ def vs_kv4_read(pool, table, lens, start, cu_seqlens, max_read, K, V, ws, stream
                              _ptr(start), B, _kv4_max(table, lens, B), Hkv, d,
                              _ptr(cu_seqlens), int(max_read), K.shape[0], _ptr(K), _ptr(V),
                              K.stride(0), _ptr(ws), ws.numel(),
-                             _stream_at(stream, K, V, pool, table, lens, ws)), "vs_kv4_read")
+                             _stream_at(stream, pool, table, lens, start, cu_seqlens, K, V, ws)),
+           "vs_kv4_read")
 
 
 def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, sinks=0,
@@ -616,7 +619,8 @@ def vs_kv4_decode_attn_fwd(Q, pool, table, lens, max_len, O, lse, ws, window=0, 
         _ptr(Q), _dtype(Q), Q.stride(0), _ptr(pool), n_pages, _ptr(table), table.stride(0),
         _ptr(lens), B, _kv4_max(table, lens, B, max_len), Hq, Hkv, d, float(softmax_scale), int(window),
         int(sinks), _ptr(acc_in), _ptr(acc_out), ld, _ptr(O), _ptr(lse), _ptr(ws), ws.numel(),
-        _stream_at(stream, Q, O, pool, table, lens, ws)), "vs_kv4_decode_attn_fwd")
+        _stream_at(stream, Q, pool, table, lens, acc_in, acc_out, O, lse, ws)),
+        "vs_kv4_decode_attn_fwd")
 
 
 def vs_kv4_evict(pool, table, lens, n_tokens, max_len, acc, pos, keep, sinks, recent, lens_out,
@@ -636,7 +640,8 @@ def vs_kv4_evict(pool, table, lens, n_tokens, max_len, acc, pos, keep, sinks, re
                               _ptr(acc), _ptr(pos), ld,
                               int(keep), int(sinks), int(recent), _ptr(lens_out), _ptr(acc_out),
                               _ptr(pos_out), ld_out, _ptr(ws), ws.numel(),
-                              _stream_at(stream, pool, table, lens, acc, pos, ws)), "vs_kv4_evict")
+                              _stream_at(stream, pool, table, lens, n_tokens, acc, pos, lens_out, acc_out,
+                                         pos_out, ws)), "vs_kv4_evict")
 
 
 def vs_read_device_status(ws, stream=None) -> tuple[int, int]:
