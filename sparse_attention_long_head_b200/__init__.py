@@ -306,6 +306,7 @@ def _window_args(Q, K, V, O, lse):
     assert O.shape == Q.shape and V.shape == K.shape and K.shape[::2] == (N, d)
     for t, like in ((Q, None), (O, Q), (K, None), (V, K)):
         _rows(t, like)
+    assert K.dtype is Q.dtype, "types must match"
     assert lse is None or _is(lse, torch.float32, (Hq, N))
 
 

@@ -83,3 +83,16 @@ def test_every_tensor_must_be_on_the_current_device(name, elsewhere, no_library)
         call(**here)
     with pytest.raises(ValueError, match="current device"):
         call(**here | {elsewhere: make()[elsewhere]})
+
+
+@pytest.mark.parametrize("name", ["window", "window, packed"])
+@pytest.mark.parametrize("other", ["K", "V", "O", "KV"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32, torch.uint8])
+def test_window_tensors_are_of_one_type(name, other, dtype, no_library):
+    """Keys of another type would be read as the queries' (bytes: out of their range)."""
+    call, make = CALLS[name]
+    args = {k: t.as_subclass(_OnDevice) for k, t in make().items()}
+    with pytest.raises(Reached):
+        call(**args)
+    with pytest.raises(AssertionError):
+        call(**args | {k: args[k].to(dtype) for k in other})
