@@ -401,7 +401,8 @@ vs_status vs_dense_attn_fwd(const void* Q, const void* K, const void* V, vs_dtyp
  * What lies outside a sequence never reaches its rows, whatever it holds.
  * Inside a sequence V must be finite: an infinity or NaN in V row j also
  * reaches rows that do not see j but share its 128-key block (its weight is
- * 0, and 0 * inf is NaN).  K may hold anything where it is not visible.
+ * 0, and 0 * inf is NaN).  K may hold anything where it is not visible; a row
+ * that sees a NaN has O = NaN and lse = NaN.
  */
 vs_status vs_window_attn_fwd(const void* Q, const void* K, const void* V, vs_dtype dtype, int N,
                              int Hq, int Hkv, int d, int64_t q_stride_tok, int64_t kv_stride_tok,

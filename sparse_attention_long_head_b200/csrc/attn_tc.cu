@@ -822,9 +822,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
       }
+      // window: a row that sees a NaN has l = NaN and is not empty, so the NaN stays
+      const bool keyed = l > 0.f || (MODE == kAttnWindow && l != l);
       if (i < ui.Nb && P.lse)
-        *lrow_of() =
-            l > 0.f ? (m_use + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        *lrow_of() = keyed ? (m_use + log2f(l)) * 0.6931471805599453f : -INFINITY;
       ++ucount;
     }
   } else if (warp == kWarpMMA) {
