@@ -208,6 +208,12 @@ def _dtype(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+def _output_like(Q):
+    """An output with the rows of Q: the calls have one row stride for both, and Q may be a slice of
+    a fused projection."""
+    return torch.empty_strided(Q.shape, Q.stride(), dtype=Q.dtype, device=Q.device)
+
+
 # ------------------------------------------------------------------ ABI
 
 
@@ -386,7 +392,7 @@ def aggregate_varlen(Q, K, V, cu_seqlens, max_seqlen, ws=None, stream=None):
     T, Hq, _ = Q.shape
     B = cu_seqlens.numel() - 1
     ws = ws if ws is not None else workspace(256, Q.device)
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=Q.device)
     wsd = workspace(vs_attn_workspace_size_varlen(B, max_seqlen, 1, Q.shape[2]), Q.device)
     vs_dense_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, O, lse, wsd, stream=stream)
@@ -461,7 +467,7 @@ def block_prefill_varlen(Q, K, V, cu_seqlens, max_seqlen, alpha, stream=None):
     ws = workspace(max(vs_block_select_workspace_size_varlen(B, max_seqlen, K.shape[1], d),
                        vs_block_attn_workspace_size_varlen(B, max_seqlen, Hq)), Q.device)
     vs_block_select_varlen(Q, K, cu_seqlens, max_seqlen, alpha, mask, ws, stream=stream)
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, total), dtype=torch.float32, device=Q.device)
     vs_block_sparse_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, mask, O, lse, ws,
                                     stream=stream)
@@ -477,7 +483,7 @@ def block_prefill(Q, K, V, alpha, stream=None):
     ws = workspace(max(vs_block_select_workspace_size(N, K.shape[1], d),
                        vs_block_attn_workspace_size(N, Hq)), Q.device)
     vs_block_select(Q, K, alpha, mask, ws, stream=stream)
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device)
     vs_block_sparse_attn_fwd(Q, K, V, mask, O, lse, ws, stream=stream)
     return O, lse, mask
@@ -677,7 +683,7 @@ def kv4_pool(n_pages: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
 def kv4_decode_attention(Q, pool, table, lens, max_len, window=0, sinks=0, ws=None, stream=None):
     """Allocates outputs and runs vs_kv4_decode_attn_fwd without weights -> (O, lse [Hq, B])."""
     B, Hq, d = Q.shape
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, B), dtype=torch.float32, device=Q.device)
     if ws is None:
         ws = workspace(vs_kv4_decode_workspace_size(B, Hq, pool.shape[1], d, max_len), Q.device)
@@ -711,7 +717,7 @@ def select_varlen(scores, cu_seqlens, max_seqlen, mode, caps, cap_max, tau=1.0, 
 
 def sparse_attention(Q, K, V, v_idx, v_cnt, s_idx, s_cnt, ws=None, with_lse=True, stream=None):
     N, Hq, d = Q.shape
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device) if with_lse else None
     if ws is None:
         ws = workspace(vs_attn_workspace_size_ld(N, Hq, v_idx.shape[0], d, v_idx.stride(0)),
@@ -722,7 +728,7 @@ def sparse_attention(Q, K, V, v_idx, v_cnt, s_idx, s_cnt, ws=None, with_lse=True
 
 def dense_attention(Q, K, V, ws=None, with_lse=True, stream=None):
     N, Hq, d = Q.shape
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device) if with_lse else None
     ws = workspace(256, Q.device) if ws is None else ws
     vs_dense_attn_fwd(Q, K, V, O, lse, ws, stream=stream)
@@ -732,7 +738,7 @@ def dense_attention(Q, K, V, ws=None, with_lse=True, stream=None):
 def window_attention(Q, K, V, window, sinks=0, ws=None, with_lse=True, stream=None):
     """Allocates outputs and runs vs_window_attn_fwd -> (O, lse)."""
     N, Hq, d = Q.shape
-    O = torch.empty_like(Q)
+    O = _output_like(Q)
     lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device) if with_lse else None
     ws = workspace(256, Q.device) if ws is None else ws
     vs_window_attn_fwd(Q, K, V, window, sinks, O, lse, ws, stream=stream)
@@ -749,7 +755,7 @@ def aggregate(Q, K, V=None, lse=None, ws=None, stream=None):
     if lse is None:
         if V is None:
             raise ValueError("V is needed to compute the LSE")
-        O = torch.empty_like(Q)
+        O = _output_like(Q)
         lse = torch.empty((Hq, N), dtype=torch.float32, device=Q.device)
         vs_dense_attn_fwd(Q, K, V, O, lse, ws, stream=stream)
         del O

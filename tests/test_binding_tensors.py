@@ -96,3 +96,54 @@ def test_window_tensors_are_of_one_type(name, other, dtype, no_library):
         call(**args)
     with pytest.raises(AssertionError):
         call(**args | {k: args[k].to(dtype) for k in other})
+
+
+# ------------------------------------------------------------------------------ allocation helpers
+
+
+class _Accepting:
+    """A library whose calls succeed without doing anything."""
+
+    def __getattr__(self, name):
+        return lambda *args: 4096 if name.endswith(("_size", "_size_ld", "_size_varlen")) else 0
+
+
+@pytest.fixture
+def accepting_library(monkeypatch):
+    monkeypatch.setattr(vs, "lib", lambda: _Accepting())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # what CPU tensors report
+    monkeypatch.setattr(vs, "_raw_stream", lambda device: 0)
+
+
+def _index():
+    return _ints(1, 8), _ints(1), _ints(1, 8), _ints(1)
+
+
+HELPERS = {
+    "window_attention": lambda Q, K, V, **kw: vs.window_attention(Q, K, V, 3, 1, **kw),
+    "kv4_decode_attention": lambda Q, K, V, **kw: vs.kv4_decode_attention(
+        Q, torch.zeros((3, HKV, 4608), dtype=torch.uint8), _ints(T, 4), _ints(T), N, **kw),
+    "dense_attention": lambda Q, K, V, **kw: vs.dense_attention(Q, K, V, **kw),
+    "sparse_attention": lambda Q, K, V, **kw: vs.sparse_attention(Q, K, V, *_index(), **kw),
+    "block_prefill": lambda Q, K, V, **kw: vs.block_prefill(Q, K, V, 0.1, **kw),
+    "block_prefill_varlen": lambda Q, K, V, **kw: vs.block_prefill_varlen(Q, K, V, _ints(B + 1), T, 0.1, **kw),
+    "aggregate": lambda Q, K, V, **kw: vs.aggregate(Q, K, V, **kw),
+    "aggregate_varlen": lambda Q, K, V, **kw: vs.aggregate_varlen(Q, K, V, _ints(B + 1), T, **kw),
+}
+
+
+@pytest.mark.parametrize("name", HELPERS)
+def test_helpers_give_the_output_the_rows_of_a_sliced_query(name, accepting_library, monkeypatch):
+    """Q as a slice of a fused projection: the calls have one row stride for Q and O, so an O with packed
+    rows would be refused, or written behind its end."""
+    fused = _bf16(T, HQ + 2 * HKV, D)
+    Q, K, V = fused[:, :HQ], fused[:, HQ:HQ + HKV], fused[:, HQ + HKV:]
+    outputs = []
+    for call in ("vs_dense_attn_fwd", "vs_dense_attn_fwd_varlen"):
+        def fwd(*args, _call=getattr(vs, call), **kw):
+            outputs.append(args[3 if _call.__name__ == "vs_dense_attn_fwd" else 5])
+            return _call(*args, **kw)
+        monkeypatch.setattr(vs, call, fwd)
+    out = HELPERS[name](Q, K, V)
+    for O in outputs or out[:1]:
+        assert O.shape == Q.shape and O.stride() == Q.stride() and O.dtype is Q.dtype
