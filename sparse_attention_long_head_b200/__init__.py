@@ -13,6 +13,7 @@ are torch CUDA tensors; layouts are those of the header (token-major
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -208,6 +209,29 @@ def _dtype(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+def _allocates(helper):
+    """For a helper whose last argument is a stream: what it allocates for a stream that is not the
+    current one comes from that stream's memory.  The current stream's may still be written by earlier
+    kernels there, and a workspace would be handed out again before the other stream has used it.  The
+    results' memory also waits for the caller's stream, which goes on to read them."""
+    place = helper.__code__.co_argcount - 1
+
+    @functools.wraps(helper)
+    def call(*args, **kwargs):
+        stream = args[place] if len(args) > place else kwargs.get("stream")
+        if stream is None:
+            return helper(*args, **kwargs)
+        caller = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            out = helper(*args, **kwargs)
+        for t in out:
+            if t is not None:
+                t.record_stream(caller)
+        return out
+
+    return call
+
+
 def _output_like(Q):
     """An output with the rows of Q: the calls have one row stride for both, and Q may be a slice of
     a fused projection."""
@@ -386,6 +410,7 @@ def vs_attn_aggregate_varlen(Q, K, cu_seqlens, max_seqlen, lse, A_v, A_s, ws, so
         ws.numel(), _stream(stream)), "vs_attn_aggregate_varlen")
 
 
+@_allocates
 def aggregate_varlen(Q, K, V, cu_seqlens, max_seqlen, ws=None, stream=None):
     """Per-sequence column / diagonal sums of a packed batch, fp32 [Hq, total]
     each: the batched dense forward for the row LSE, then the aggregation."""
@@ -457,6 +482,7 @@ def vs_block_sparse_attn_fwd_varlen(Q, K, V, cu_seqlens, max_seqlen, mask, O, ls
         ws.numel(), _stream(stream)), "vs_block_sparse_attn_fwd_varlen")
 
 
+@_allocates
 def block_prefill_varlen(Q, K, V, cu_seqlens, max_seqlen, alpha, stream=None):
     """Batched block prefill: discovery then block-sparse attention per
     sequence; returns (O, lse [Hq, total], mask [B, Hq, T, W])."""
@@ -474,6 +500,7 @@ def block_prefill_varlen(Q, K, V, cu_seqlens, max_seqlen, alpha, stream=None):
     return O, lse, mask
 
 
+@_allocates
 def block_prefill(Q, K, V, alpha, stream=None):
     """FlashPrefill-style pattern discovery then block-sparse attention:
     returns (O, lse, mask)."""
@@ -680,6 +707,7 @@ def kv4_pool(n_pages: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
     return torch.empty((n_pages, Hkv, vs_kv4_page_bytes(1, d)), dtype=torch.uint8, device=device)
 
 
+@_allocates
 def kv4_decode_attention(Q, pool, table, lens, max_len, window=0, sinks=0, ws=None, stream=None):
     """Allocates outputs and runs vs_kv4_decode_attn_fwd without weights -> (O, lse [Hq, B])."""
     B, Hq, d = Q.shape
@@ -691,6 +719,7 @@ def kv4_decode_attention(Q, pool, table, lens, max_len, window=0, sinks=0, ws=No
     return O, lse
 
 
+@_allocates
 def select(scores, mode, k_or_cap, tau=1.0, ws=None, stream=None):
     """Allocates outputs and runs vs_select -> (idx [H, k_or_cap], count [H])."""
     H, N = scores.shape
@@ -701,6 +730,7 @@ def select(scores, mode, k_or_cap, tau=1.0, ws=None, stream=None):
     return idx, cnt
 
 
+@_allocates
 def select_varlen(scores, cu_seqlens, max_seqlen, mode, caps, cap_max, tau=1.0, ws=None,
                   stream=None):
     """Allocates outputs and runs vs_select_varlen -> (idx [B * H, cap_max] filled with -1 past
@@ -715,6 +745,7 @@ def select_varlen(scores, cu_seqlens, max_seqlen, mode, caps, cap_max, tau=1.0, 
     return idx, cnt
 
 
+@_allocates
 def sparse_attention(Q, K, V, v_idx, v_cnt, s_idx, s_cnt, ws=None, with_lse=True, stream=None):
     N, Hq, d = Q.shape
     O = _output_like(Q)
@@ -726,6 +757,7 @@ def sparse_attention(Q, K, V, v_idx, v_cnt, s_idx, s_cnt, ws=None, with_lse=True
     return O, lse
 
 
+@_allocates
 def dense_attention(Q, K, V, ws=None, with_lse=True, stream=None):
     N, Hq, d = Q.shape
     O = _output_like(Q)
@@ -735,6 +767,7 @@ def dense_attention(Q, K, V, ws=None, with_lse=True, stream=None):
     return O, lse
 
 
+@_allocates
 def window_attention(Q, K, V, window, sinks=0, ws=None, with_lse=True, stream=None):
     """Allocates outputs and runs vs_window_attn_fwd -> (O, lse)."""
     N, Hq, d = Q.shape
@@ -745,6 +778,7 @@ def window_attention(Q, K, V, window, sinks=0, ws=None, with_lse=True, stream=No
     return O, lse
 
 
+@_allocates
 def aggregate(Q, K, V=None, lse=None, ws=None, stream=None):
     """Ground-truth column / diagonal sums (A_v, A_s), fp32 [Hq, N] each.
 

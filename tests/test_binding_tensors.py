@@ -147,3 +147,51 @@ def test_helpers_give_the_output_the_rows_of_a_sliced_query(name, accepting_libr
     out = HELPERS[name](Q, K, V)
     for O in outputs or out[:1]:
         assert O.shape == Q.shape and O.stride() == Q.stride() and O.dtype is Q.dtype
+
+
+@pytest.mark.parametrize("name,positional", [(n, False) for n in (*HELPERS, "select", "select_varlen")] +
+                         [("window_attention", True), ("select", True)])
+def test_helpers_allocate_on_the_stream_of_the_call(name, positional, accepting_library, monkeypatch):
+    """What a helper allocates for another stream's call comes from that stream's memory: the current
+    stream's may still be written by its earlier kernels, and is handed out again when the helper
+    returns, before the other stream has run."""
+    current, side = object(), type("Stream", (), {"cuda_stream": 77})()
+    state = {"now": current}
+    allocated, recorded = [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, state["now"] = state["now"], self.stream
+
+        def __exit__(self, *exc):
+            state["now"] = self.before
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: state["now"])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s)))
+    for alloc in ("empty", "empty_strided", "full"):
+        def make(*args, _make=getattr(torch, alloc), **kw):
+            allocated.append(state["now"])
+            return _make(*args, **kw)
+        monkeypatch.setattr(torch, alloc, make)
+    q, k = torch.zeros((T, HQ, D), dtype=torch.bfloat16), torch.zeros((T, HKV, D), dtype=torch.bfloat16)
+    scores = torch.zeros((HQ, T))
+    select = {"select": lambda **kw: vs.select(scores, 0, 3, **kw),
+              "select_varlen": lambda **kw: vs.select_varlen(scores, _ints(B + 1), T, 0, _ints(B), 3, **kw)}
+    if positional:
+        run = {"window_attention": lambda: vs.window_attention(q, k, k, 3, 1, None, True, side),
+               "select": lambda: vs.select(scores, 0, 3, 1.0, None, side)}[name]
+    else:
+        run = (lambda: select[name](stream=side)) if name in select else lambda: HELPERS[name](q, k, k, stream=side)
+    out = run()
+    assert allocated and all(s is side for s in allocated)
+    # the caller's stream reads the results, so their memory waits for it too
+    assert {p for p, s in recorded if s is current} >= {t.data_ptr() for t in out}
+    assert state["now"] is current
+    del allocated[:], recorded[:]
+    if not positional:
+        select[name]() if name in select else HELPERS[name](q, k, k)
+        assert allocated and all(s is current for s in allocated) and not recorded

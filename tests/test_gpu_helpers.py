@@ -1,4 +1,6 @@
-"""The allocation helpers on the GPU: queries sliced out of a fused projection."""
+"""The allocation helpers on the GPU: queries sliced out of a fused projection, calls on another stream."""
+import functools
+
 import pytest
 import torch
 
@@ -15,15 +17,18 @@ def _fused(n):
     return x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:]
 
 
+@functools.cache  # kept: a call on another stream needs its inputs until it has run
 def _ints(*v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
+@functools.cache
 def _rows(n, step):
     idx = torch.arange(0, n, step, dtype=torch.int32, device="cuda").view(1, -1)
     return idx, _ints(idx.shape[1])
 
 
+@functools.cache
 def _cache():
     gen = torch.Generator("cuda").manual_seed(3)
     pool = torch.randint(0, 256, (40, HKV, 4608), dtype=torch.uint8, device="cuda", generator=gen)
@@ -57,3 +62,23 @@ def test_sliced_queries_give_what_packed_ones_give(name, cuda_device):
     got = HELPERS[name](Q, K, V)
     for a, b in zip(got, want):
         assert _close(name, a, b)
+
+
+@pytest.mark.parametrize("name", HELPERS)
+def test_calls_on_a_busy_stream_keep_their_memory(name, cuda_device):
+    """The call waits on its own stream while the current one allocates and fills what is free there."""
+    Q, K, V = _fused(N)
+    want = HELPERS[name](Q, K, V)
+    sizes = [256, 4096, 1 << 20, 2 << 20, 8 << 20] + [t.untyped_storage().nbytes() for t in want]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # some 10 ms
+        got = HELPERS[name](Q, K, V, stream=side)
+        for n in 3 * sizes:
+            torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(got, want):
+            assert _close(name, a, b)
+        del got
