@@ -565,7 +565,7 @@ vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64
  *            NULL) bytes, 256-byte aligned (the size depends on the current
  *            device's SM count; with weights it includes one float per query
  *            head and slot).
- * VS_ERR_UNSUPPORTED where the pages of all rows do not fit 32 bits.
+ * VS_ERR_UNSUPPORTED where the pages of all rows come within 2^16 of 2^31.
  */
 size_t vs_kv4_decode_workspace_size(int B, int Hq, int Hkv, int d, int max_len, int with_weights);
 vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride_tok,

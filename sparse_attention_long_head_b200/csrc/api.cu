@@ -524,7 +524,7 @@ static vs_status window_impl(const void* Q, const void* K, const void* V, vs_dty
   if (dtype != VS_BF16) return VS_ERR_UNSUPPORTED;
   const PlanLayout L = PlanLayout::make(N, 1);  // tile and pair counts
   // units (sequence, head, pair of query blocks) are counted in 32 bits
-  if ((int64_t)B * Hq * L.P >= ((int64_t)1 << 31)) return VS_ERR_UNSUPPORTED;
+  if ((int64_t)B * Hq * L.P >= kMaxCount) return VS_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < kStatusBytes || !aligned(ws, 256)) return VS_ERR_WORKSPACE;
   AttnArgs a{};
   a.Q = Q;
@@ -692,7 +692,7 @@ vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride
     return VS_ERR_UNSUPPORTED;
   // pages of all rows are counted in 32 bits
   const int64_t rows = (int64_t)B * Hkv * ((Hq / Hkv + 7) / 8);
-  if (Hq > (1 << 20) || rows * ((max_len + 63LL) / 64) >= ((int64_t)1 << 31))
+  if (Hq > (1 << 20) || rows * ((max_len + 63LL) / 64) >= kMaxCount)
     return VS_ERR_UNSUPPORTED;
   if (ws_bytes < vs_kv4_decode_workspace_size(B, Hq, Hkv, d, max_len, acc_out != nullptr))
     return VS_ERR_WORKSPACE;

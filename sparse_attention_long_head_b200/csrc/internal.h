@@ -12,6 +12,9 @@ namespace vs {
 
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
 constexpr size_t kStatusBytes = 256;                      // status word + padding
+// Work items are counted in int and dealt out in steps of the grid: counts stay
+// below this, so that the last step cannot pass 2^31.
+constexpr int64_t kMaxCount = ((int64_t)1 << 31) - (1 << 16);
 
 inline int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
