@@ -398,6 +398,10 @@ vs_status vs_dense_attn_fwd(const void* Q, const void* K, const void* V, vs_dtyp
  *            the last sequence are left as they were).
  *   ws       at least 256 bytes, 256-byte aligned (status word).
  * VS_BF16 only (else VS_ERR_UNSUPPORTED); 1 <= N <= 2^24.
+ * Scores, maxima, sums and O are held in fp32; the weights are rounded to bf16
+ * for their product with V (as in every bf16 attention of this library): O is
+ * off by up to 2^-8 max |V| from that, and by 2^-8 of itself from its own
+ * rounding.  lse does not depend on the rounded weights.
  * What lies outside a sequence never reaches its rows, whatever it holds.
  * Inside a sequence V must be finite: an infinity or NaN in V row j also
  * reaches rows that do not see j but share its 128-key block (its weight is
@@ -557,8 +561,13 @@ vs_status vs_kv4_read(const void* pool, int n_pages, const int32_t* table, int64
  *            acc_out itself, or NULL (zeros).  ld >= max_len.  Entries from
  *            lens[b] on are left as they were.
  *   lse      fp32 [Hq][B] (output) or NULL.
- * The values' steps s are expected in [2^-40, 2^40] and |Q| below 2^113; beyond
- * that results lose precision or overflow.
+ * Scores, maxima, sums, weights (acc) and O are held in fp32; only the products
+ * of a weight and a step s are rounded to bf16 for their product with the codes
+ * (counted from 8): O is off by up to 2^-8 8 max s from that, and by 2^-8 of
+ * itself from its own rounding.
+ * The values' steps s are expected to be 0 or in [2^-40, 2^40] and their minima
+ * m below 2^44 in size, |Q| below 2^113 and softmax_scale |Q| below 2^112;
+ * beyond that results lose precision or overflow.
  * A sequence without slots gives O = 0 and LSE = -inf.  Results do not depend
  * on timing: repeated calls give the same bits on the same device.
  *   ws       vs_kv4_decode_workspace_size(B, Hq, Hkv, d, max_len, acc_out !=
@@ -583,7 +592,8 @@ vs_status vs_kv4_decode_attn_fwd(const void* Q, vs_dtype dtype, int64_t q_stride
  * below k that goes is overwritten by the i-th slot at or above k that stays.
  * Every head keeps its own tokens.
  *   lens, acc, pos   as vs_kv4_append and vs_kv4_decode_attn_fwd leave them,
- *            rows of length ld >= max_len; n_tokens as for vs_kv4_append.
+ *            rows of length ld >= max_len; n_tokens as for vs_kv4_append, but
+ *            not NULL.
  *   keep, sinks, recent   keep >= 1, sinks >= 0, recent >= 0, sinks + recent
  *            <= keep.
  *   lens_out int32 [B], acc_out, pos_out [B][Hkv][ld_out], ld_out >=

@@ -54,7 +54,8 @@ constexpr int kDecMaxWarps = 12;
 
 // The weights carry 2^kShift (up to 2^8 more while the running maximum lags):
 // V steps s from 2^-40 (below, the products with codes of 2^-133 lose bits) to
-// 2^40 (above, 2^56 15 s summed over 2^24 slots overflows).
+// 2^40, and minima m below 2^44 (above, 2^56 (15 s + m) summed over 2^24 slots
+// overflows).
 constexpr float kShift = 48.f;
 constexpr int kDecMinPages = 12;  // per CTA, where the list is short
 
