@@ -11,14 +11,16 @@
 //
 // Two kernels.  The first finds who stays, one cluster of 1 to 8 CTAs a row: each
 // thread keeps up to 32 slots of the row as order-preserving 32-bit keys in
-// registers, the boundary key is found digit by digit (four of 8 bits) over
+// registers (at 32 of them some 25 words a thread go through local memory once),
+// the boundary key is found digit by digit (four of 8 bits) over
 // histograms that the cluster sums through distributed shared memory, and
 // ballots in slot order give the lists of holes and of the slots that fill
 // them.  Bound by latency (some ten cluster barriers and the row read once, 8
 // bytes a slot).  The second moves, 16 lanes a move over the whole device.
-// 256 rows of 4352 slots cut to 4096 take 27 us, 16 rows of 100,000 to 131,072
-// slots cut to 8192 take 60 us (123,000 moves of 144 bytes in pieces of 32 and
-// 4); by themselves 16 and 16 (three dependent loads a move), 36 and 27.
+// On new data 256 rows of 4200 to 4352 slots cut to 4096 take 34 us, 16 rows of
+// 100,000 to 131,072 slots cut to 8192 take 63 to 65 us (123,000 moves of 144
+// bytes in pieces of 32 and 4); by themselves the kernels take 16 and 16 (three
+// dependent loads a move), 36 and 27.  Data that L2 still holds: 27 and 60 in all.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
