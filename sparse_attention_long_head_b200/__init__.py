@@ -221,6 +221,8 @@ def _allocates(helper):
         stream = args[place] if len(args) > place else kwargs.get("stream")
         if stream is None:
             return helper(*args, **kwargs)
+        if stream.device_index != torch.cuda.current_device():  # entering it would change the device
+            raise ValueError("the stream is not on the current device")
         caller = torch.cuda.current_stream()
         with torch.cuda.stream(stream):
             out = helper(*args, **kwargs)

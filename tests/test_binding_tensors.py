@@ -155,7 +155,7 @@ def test_helpers_allocate_on_the_stream_of_the_call(name, positional, accepting_
     """What a helper allocates for another stream's call comes from that stream's memory: the current
     stream's may still be written by its earlier kernels, and is handed out again when the helper
     returns, before the other stream has run."""
-    current, side = object(), type("Stream", (), {"cuda_stream": 77})()
+    current, side = object(), type("Stream", (), {"cuda_stream": 77, "device_index": -1})()
     state = {"now": current}
     allocated, recorded = [], []
 
@@ -195,3 +195,13 @@ def test_helpers_allocate_on_the_stream_of_the_call(name, positional, accepting_
     if not positional:
         select[name]() if name in select else HELPERS[name](q, k, k)
         assert allocated and all(s is current for s in allocated) and not recorded
+
+
+@pytest.mark.parametrize("name", HELPERS)
+def test_helpers_refuse_a_stream_of_another_device(name, accepting_library, monkeypatch):
+    """Taking over the stream's device would run kernels there on this device's tensors."""
+    elsewhere = type("Stream", (), {"cuda_stream": 77, "device_index": 1})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *device: object())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: pytest.fail("the stream was entered"))
+    with pytest.raises(ValueError, match="current device"):
+        HELPERS[name](_bf16(T, HQ, D), _bf16(T, HKV, D), _bf16(T, HKV, D), stream=elsewhere)
