@@ -591,8 +591,9 @@ def _kv4_rows(t, dtype, B, Hkv, need=0):
     if t.is_contiguous():
         return ld
     sb, sh, s1 = t.stride()
-    assert need <= ld <= sh and (ld <= 1 or s1 == 1) and (B <= 1 or sb == Hkv * sh)
-    return sh if B * Hkv > 1 else ld
+    row = sh if Hkv > 1 else sb if B > 1 else ld  # a size of 1 has no step
+    assert need <= ld <= row and (ld <= 1 or s1 == 1) and (B <= 1 or sb == Hkv * row)
+    return row
 
 
 def vs_kv4_append(K, V, cu_seqlens, max_new, pool, table, lens, ws, n_tokens=None, A_v=None,

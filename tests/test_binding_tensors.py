@@ -205,3 +205,19 @@ def test_helpers_refuse_a_stream_of_another_device(name, accepting_library, monk
     monkeypatch.setattr(torch.cuda, "stream", lambda s: pytest.fail("the stream was entered"))
     with pytest.raises(ValueError, match="current device"):
         HELPERS[name](_bf16(T, HQ, D), _bf16(T, HKV, D), _bf16(T, HKV, D), stream=elsewhere)
+
+
+def test_rows_of_one_kv_head_may_be_slices_of_longer_ones():
+    """Of a size of 1 the stride says nothing: the row length is that of the other dimension."""
+    wide = torch.zeros((3, 40))
+    one_head, one_sequence = wide[:, :30].unsqueeze(1), wide[:, :30].unsqueeze(0)
+    assert vs._kv4_rows(one_head, torch.float32, 3, 1, 30) == 40
+    assert vs._kv4_rows(one_sequence, torch.float32, 1, 3, 30) == 40
+    assert vs._kv4_rows(wide[:1, :30].unsqueeze(0), torch.float32, 1, 1, 30) == 30
+    assert vs._kv4_rows(torch.zeros((3, 2, 40))[..., :30], torch.float32, 3, 2, 30) == 40
+    for bad in (wide[:, :30].t()[:3].unsqueeze(1),                   # entries of a row apart
+                wide[:1].expand(3, 40)[:, :30].unsqueeze(1),         # rows that are one row
+                torch.zeros((3, 5, 40))[:, ::2, :30]):               # heads and sequences of different steps
+        with pytest.raises(AssertionError):
+            vs._kv4_rows(bad, torch.float32, *bad.shape[:2], bad.shape[2])
+    assert vs._kv4_rows(torch.zeros((3, 4, 40))[:, :1, :30], torch.float32, 3, 1, 30) == 160
