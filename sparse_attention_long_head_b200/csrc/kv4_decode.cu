@@ -19,7 +19,7 @@
 //
 // Its floor is the cache's bytes: 72 per slot, KV head and group (64 codes and
 // pairs of K and V), at G = Hq / Hkv query heads each.  4 sequences of 120,000
-// to 131,072 slots, 32/8 heads, d = 128 take 121 us on new data (4.8 TB/s, 73% of
+// to 131,072 slots, 32/8 heads, d = 128 take 116 to 121 us on new data (73 to 76% of
 // a copy; 109 us where the same cache is read again and L2 still holds a part);
 // what bounds it there is instructions, 217 per 16 slots: the ALU pipe is busy
 // 54% of the cycles and an issue slot 50%, with three warps a scheduler.  mma.sync m16n8k16 is
